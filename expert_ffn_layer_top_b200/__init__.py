@@ -17,10 +17,15 @@ from ._lib import (  # noqa: F401
     moe_dequantize,
     moe_device_error,
     moe_grouped_ffn,
+    moe_grouped_gemm,
+    moe_grouped_gemm_dgrad,
+    moe_grouped_gemm_fp8,
+    moe_grouped_gemm_wgrad,
     moe_layer_forward,
     moe_permute,
     moe_permute_static,
     moe_prepack,
+    moe_quantize_fp8,
     moe_selftest_wait,
     moe_tensor_peak_tflops,
     moe_set_wait_limit_ns,

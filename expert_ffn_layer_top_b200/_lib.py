@@ -1,6 +1,7 @@
 """ctypes binding of libmoe.so. Argument marshalling only (see include/moe.h)."""
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 import threading
@@ -76,6 +77,17 @@ def lib():
             L.moe_combine.argtypes = [_P, _I, _P, _P, _I, _I, _I, _P, _P]
             L.moe_dequantize.restype = st
             L.moe_dequantize.argtypes = [_I, _P, _P, C.c_float, _I, _I, _P, _P]
+            i64 = C.c_int64
+            L.moe_grouped_gemm.restype = st
+            L.moe_grouped_gemm.argtypes = [_P, i64, _I, _P, _P, i64, i64, _I, _I, _I, _P, i64, _I, _P]
+            L.moe_grouped_gemm_dgrad.restype = st
+            L.moe_grouped_gemm_dgrad.argtypes = [_P, i64, _I, _P, _P, i64, i64, _I, _I, _I, _P, i64, _I, _P]
+            L.moe_grouped_gemm_wgrad.restype = st
+            L.moe_grouped_gemm_wgrad.argtypes = [_P, i64, _P, i64, _I, _P, _I, _I, _I, _P, i64, i64, _I, _I, _P]
+            L.moe_quantize_fp8.restype = st
+            L.moe_quantize_fp8.argtypes = [_P, i64, _I, _I, _I, _P, i64, _P, _P]
+            L.moe_grouped_gemm_fp8.restype = st
+            L.moe_grouped_gemm_fp8.argtypes = [_P, i64, _P, _I, _P, _P, i64, i64, _P, i64, _I, _I, _I, _P, i64, _I, _P]
             L.moe_layer_forward.restype = st
             L.moe_layer_forward.argtypes = [_P, _I, _P, _I, _P, _I, C.POINTER(_Experts), _I, _P, _I, _I, _P, _P,
                                             _P, _P, C.c_size_t, _P]
@@ -303,6 +315,150 @@ def moe_dequantize(fmt: str, w: torch.Tensor, scale: Optional[torch.Tensor], tsc
     out = torch.empty(rows, K, dtype=torch.bfloat16, device=w.device)
     _check(lib().moe_dequantize(FMT[fmt], _ptr(w), _ptr(scale), float(tscale), rows, K, _ptr(out), _stream()))
     return out
+
+
+_FP8 = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _on(*ts: Optional[torch.Tensor]):
+    """The tensors' device, made current while the library is called."""
+    _need_cuda(*ts)
+    dev = next(t.device for t in ts if t is not None)
+    if any(t is not None and t.device != dev for t in ts):
+        raise ValueError("tensors on one device expected")
+    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else contextlib.nullcontext()
+
+
+def _matrix(name: str, t: torch.Tensor, dtypes, ndim: int = 2):
+    if t.dtype not in dtypes or t.dim() != ndim:
+        raise ValueError(f"{name}: expected {ndim}-D {' or '.join(str(d) for d in dtypes)}, got {t.dim()}-D {t.dtype}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Elements from row to row of a matrix (of each of a batch); a lone row's stride says nothing."""
+    return t.stride(-2) if t.shape[-2] > 1 else -(-t.shape[-1] // 16) * 16
+
+
+def _estride(t: torch.Tensor) -> int:
+    if t.shape[0] > 1 and t.stride(0) == 0:   # 0 means dense in the C ABI
+        raise ValueError("experts expanded from one: pass a copy per expert")
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _offsets(offsets: Optional[torch.Tensor], E: int):
+    if offsets is None:
+        if E != 1:
+            raise ValueError("offsets: needed with more than one expert")
+    elif offsets.dtype != torch.int32 or offsets.shape != (E + 1,) or not offsets.is_contiguous():
+        raise ValueError(f"offsets: expected contiguous int32 [{E + 1}]")
+
+
+def _result(out: Optional[torch.Tensor], shape, fp32: bool, device) -> torch.Tensor:
+    dtype = torch.float32 if fp32 else torch.bfloat16
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"out: expected shape {tuple(shape)}, got {tuple(out.shape)}")
+    _matrix("out", out, (dtype,), len(shape))
+    return out
+
+
+def _experts_of(w: torch.Tensor) -> torch.Tensor:
+    return w.unsqueeze(0) if w.dim() == 2 else w
+
+
+def moe_grouped_gemm(x: torch.Tensor, offsets: Optional[torch.Tensor], w: torch.Tensor, y_fp32: bool = False,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[r] = w[e] x[r] for the rows r of expert e; w bf16 [E, N, K] (or [N, K] with offsets None)."""
+    w = _experts_of(w)
+    _matrix("x", x, (torch.bfloat16,))
+    _matrix("w", w, (torch.bfloat16,), 3)
+    E, N, K = w.shape
+    if x.shape[1] != K:
+        raise ValueError(f"x has {x.shape[1]} columns, w {K}")
+    _offsets(offsets, E)
+    with _on(x, offsets, w, out):
+        y = _result(out, (x.shape[0], N), y_fp32, x.device)
+        _check(lib().moe_grouped_gemm(_ptr(x), _ld(x), x.shape[0], _ptr(offsets), _ptr(w), _ld(w), _estride(w), E, N, K,
+                                      _ptr(y), _ld(y), int(y_fp32), _stream()))
+    return y
+
+
+def moe_grouped_gemm_dgrad(dy: torch.Tensor, offsets: Optional[torch.Tensor], w: torch.Tensor, dx_fp32: bool = False,
+                           out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dx[r] = w[e]^T dy[r]: the gradient of moe_grouped_gemm for x."""
+    w = _experts_of(w)
+    _matrix("dy", dy, (torch.bfloat16,))
+    _matrix("w", w, (torch.bfloat16,), 3)
+    E, N, K = w.shape
+    if dy.shape[1] != N:
+        raise ValueError(f"dy has {dy.shape[1]} columns, w {N} rows")
+    _offsets(offsets, E)
+    with _on(dy, offsets, w, out):
+        dx = _result(out, (dy.shape[0], K), dx_fp32, dy.device)
+        _check(lib().moe_grouped_gemm_dgrad(_ptr(dy), _ld(dy), dy.shape[0], _ptr(offsets), _ptr(w), _ld(w), _estride(w),
+                                            E, N, K, _ptr(dx), _ld(dx), int(dx_fp32), _stream()))
+    return dx
+
+
+def moe_grouped_gemm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: Optional[torch.Tensor], dw_fp32: bool = True,
+                           out: Optional[torch.Tensor] = None, accumulate: bool = False) -> torch.Tensor:
+    """dw[e] = sum of dy[r] x[r]^T over the rows of expert e: the gradient of moe_grouped_gemm for w
+    ([E, N, K]; E = 1 with offsets None). accumulate adds to `out`."""
+    _matrix("dy", dy, (torch.bfloat16,))
+    _matrix("x", x, (torch.bfloat16,))
+    if x.shape[0] != dy.shape[0]:
+        raise ValueError(f"dy has {dy.shape[0]} rows, x {x.shape[0]}")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    E = 1 if offsets is None else offsets.numel() - 1
+    N, K = dy.shape[1], x.shape[1]
+    _offsets(offsets, E)
+    with _on(dy, x, offsets, out):
+        dw = _result(out, (E, N, K), dw_fp32, x.device)
+        _check(lib().moe_grouped_gemm_wgrad(_ptr(dy), _ld(dy), _ptr(x), _ld(x), x.shape[0], _ptr(offsets), E, N, K,
+                                            _ptr(dw), _ld(dw), _estride(dw), int(dw_fp32), int(accumulate), _stream()))
+    return dw
+
+
+def moe_quantize_fp8(x: torch.Tensor, swiglu: bool = False):
+    """(E4M3 codes uint8 [rows, K], fp32 scales [rows, ceil(K/128)]) of bf16 rows x [rows, K], or of
+    silu(gate) * up of x [rows, 2K] with swiglu."""
+    _matrix("x", x, (torch.bfloat16,))
+    if swiglu and x.shape[1] % 2:
+        raise ValueError("x: gate and up halves expected")
+    rows, K = x.shape[0], x.shape[1] // 2 if swiglu else x.shape[1]
+    with _on(x):
+        codes = torch.empty(rows, K, dtype=torch.uint8, device=x.device)
+        scale = torch.empty(rows, -(-K // 128), dtype=torch.float32, device=x.device)
+        _check(lib().moe_quantize_fp8(_ptr(x), _ld(x), rows, K, int(swiglu), _ptr(codes), K, _ptr(scale), _stream()))
+    return codes, scale
+
+
+def moe_grouped_gemm_fp8(xq: torch.Tensor, xs: torch.Tensor, offsets: Optional[torch.Tensor], wq: torch.Tensor,
+                         ws: torch.Tensor, y_fp32: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_grouped_gemm of E4M3 operands with fp32 scales per 128 of K: xq [rows, K], xs
+    [rows, ceil(K/128)], wq [E, N, K], ws [E, N, ceil(K/128)] (wq and ws without E with offsets None)."""
+    wq, ws = _experts_of(wq), _experts_of(ws)
+    _matrix("xq", xq, _FP8)
+    _matrix("wq", wq, _FP8, 3)
+    E, N, K = wq.shape
+    KB = -(-K // 128)
+    if xq.shape[1] != K:
+        raise ValueError(f"xq has {xq.shape[1]} columns, wq {K}")
+    if xs.dtype != torch.float32 or xs.shape != (xq.shape[0], KB) or not xs.is_contiguous():
+        raise ValueError(f"xs: expected contiguous float32 [{xq.shape[0]}, {KB}]")
+    if ws.dtype != torch.float32 or ws.shape != (E, N, KB) or (E > 0 and not ws[0].is_contiguous()):
+        raise ValueError(f"ws: expected float32 [{E}, {N}, {KB}], dense per expert")
+    _offsets(offsets, E)
+    with _on(xq, xs, offsets, wq, ws, out):
+        y = _result(out, (xq.shape[0], N), y_fp32, xq.device)
+        _check(lib().moe_grouped_gemm_fp8(_ptr(xq), _ld(xq), _ptr(xs), xq.shape[0], _ptr(offsets), _ptr(wq), _ld(wq),
+                                          _estride(wq), _ptr(ws), _estride(ws), E, N, K, _ptr(y), _ld(y), int(y_fp32),
+                                          _stream()))
+    return y
 
 
 def moe_layer_forward(x: torch.Tensor, wr: torch.Tensor, k: int, experts: Experts,

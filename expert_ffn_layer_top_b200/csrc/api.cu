@@ -518,6 +518,47 @@ moe_status cache_resolve_and_map(struct expert_cache *c, int layer, const int32_
 void cache_compute_end(struct expert_cache *c, cudaStream_t st);
 int cache_layout(const struct expert_cache *c);
 
+// ------------------------------------------------------------------ checks of the grouped products
+
+constexpr int kMaxProductDim = 1 << 24;
+
+static moe_status check_product(int E, int N, int K, int n_rows, const int32_t *offsets) {
+    if (E < 1 || E > kMaxExperts) return set_error(MOE_ERR_UNSUPPORTED, "E=%d outside 1..%d", E, kMaxExperts);
+    if (N < 1 || K < 1 || n_rows < 0) return set_error(MOE_ERR_INVALID_ARG, "bad N=%d, K=%d or n_rows=%d", N, K, n_rows);
+    if (N > kMaxProductDim || K > kMaxProductDim || n_rows > (1 << 30))
+        return set_error(MOE_ERR_UNSUPPORTED, "N=%d, K=%d or n_rows=%d too large", N, K, n_rows);
+    if (!offsets && E != 1) return set_error(MOE_ERR_INVALID_ARG, "offsets is NULL with E=%d experts", E);
+    if (misaligned(offsets, 4)) return set_error(MOE_ERR_INVALID_ARG, "offsets must be 4-byte aligned");
+    return MOE_OK;
+}
+
+// A matrix that the kernels read through tensor maps: esz bytes an element, `cols` used of
+// each row of ld elements.
+static moe_status check_operand(const char *what, const void *p, int64_t cols, int64_t ld, int esz) {
+    if (!p) return set_error(MOE_ERR_INVALID_ARG, "%s is NULL", what);
+    if (misaligned(p, 16)) return set_error(MOE_ERR_INVALID_ARG, "%s must be 16-byte aligned", what);
+    if (ld < cols || ld * esz % 16 || ld > (int64_t)1 << 36)
+        return set_error(MOE_ERR_INVALID_ARG, "%s: row stride %lld must be at least %lld and a multiple of 16 bytes",
+                         what, (long long)ld, (long long)cols);
+    return MOE_OK;
+}
+
+// Elements from one expert to the next; 0 becomes the dense stride.
+static moe_status check_estride(int64_t *estride, int E, int64_t rows, int64_t cols, int64_t ld, int multiple) {
+    if (*estride == 0 || E == 1) *estride = rows * ld;
+    if (*estride < (rows - 1) * ld + cols || *estride % multiple || *estride > (int64_t)1 << 38)
+        return set_error(MOE_ERR_INVALID_ARG, "expert stride %lld must hold an expert's %lld rows and be a multiple of %d",
+                         (long long)*estride, (long long)rows, multiple);
+    return MOE_OK;
+}
+
+static moe_status check_result(const void *p, int64_t cols, int64_t ld, int fp32) {
+    if (!p) return set_error(MOE_ERR_INVALID_ARG, "the result is NULL");
+    if (misaligned(p, fp32 ? 4 : 2)) return set_error(MOE_ERR_INVALID_ARG, "the result must be aligned to its elements");
+    if (ld < cols) return set_error(MOE_ERR_INVALID_ARG, "result: row stride %lld below %lld", (long long)ld, (long long)cols);
+    return MOE_OK;
+}
+
 // A kernel that waits, with the bounded wait of the FFN kernels, on an mbarrier that
 // nothing completes; no copy or MMA is in flight. The wait gives up, flags error 1 and
 // the kernel returns.
@@ -638,6 +679,88 @@ moe_status moe_grouped_ffn(const void *x_perm, int n_rows, const int32_t *offset
         return mx_ffn_impl(x_perm, 0, nullptr, 1, n_rows, offsets, experts, y_perm, y_is_fp32, ws,
                            (cudaStream_t)stream);
     return grouped_ffn_impl(x_perm, n_rows, offsets, experts, y_perm, y_is_fp32, ws, (cudaStream_t)stream);
+}
+
+moe_status moe_grouped_gemm(const void *x, int64_t ldx, int n_rows, const int32_t *offsets, const void *w,
+                            int64_t ldw, int64_t w_estride, int E, int N, int K, void *y, int64_t ldy, int y_is_fp32,
+                            moe_stream_t stream) {
+    moe_status r = check_product(E, N, K, n_rows, offsets);
+    if (r != MOE_OK || n_rows == 0) return r;
+    if ((r = check_operand("x", x, K, ldx, 2)) != MOE_OK) return r;
+    if ((r = check_operand("w", w, K, ldw, 2)) != MOE_OK) return r;
+    if ((r = check_estride(&w_estride, E, N, K, ldw, 8)) != MOE_OK) return r;
+    if ((r = check_result(y, N, ldy, y_is_fp32)) != MOE_OK) return r;
+    GemmArgs a{kGemmOpForward, E, N, K, n_rows, offsets, x, ldx, w, ldw, w_estride, nullptr, nullptr, 0,
+               y, ldy, 0, y_is_fp32, 0};
+    return launch_grouped_gemm(a, num_sms(current_device()), (cudaStream_t)stream);
+}
+
+moe_status moe_grouped_gemm_dgrad(const void *dy, int64_t lddy, int n_rows, const int32_t *offsets, const void *w,
+                                  int64_t ldw, int64_t w_estride, int E, int N, int K, void *dx, int64_t lddx,
+                                  int dx_is_fp32, moe_stream_t stream) {
+    moe_status r = check_product(E, N, K, n_rows, offsets);
+    if (r != MOE_OK || n_rows == 0) return r;
+    if ((r = check_operand("dy", dy, N, lddy, 2)) != MOE_OK) return r;
+    if ((r = check_operand("w", w, K, ldw, 2)) != MOE_OK) return r;
+    if ((r = check_estride(&w_estride, E, N, K, ldw, 8)) != MOE_OK) return r;
+    if ((r = check_result(dx, K, lddx, dx_is_fp32)) != MOE_OK) return r;
+    GemmArgs a{kGemmOpDgrad, E, N, K, n_rows, offsets, dy, lddy, w, ldw, w_estride, nullptr, nullptr, 0,
+               dx, lddx, 0, dx_is_fp32, 0};
+    return launch_grouped_gemm(a, num_sms(current_device()), (cudaStream_t)stream);
+}
+
+moe_status moe_grouped_gemm_wgrad(const void *dy, int64_t lddy, const void *x, int64_t ldx, int n_rows,
+                                  const int32_t *offsets, int E, int N, int K, void *dw, int64_t lddw,
+                                  int64_t dw_estride, int dw_is_fp32, int accumulate, moe_stream_t stream) {
+    moe_status r = check_product(E, N, K, n_rows, offsets);
+    if (r != MOE_OK) return r;
+    if (accumulate && !dw_is_fp32) return set_error(MOE_ERR_UNSUPPORTED, "dw is accumulated in fp32 only");
+    if ((r = check_result(dw, K, lddw, dw_is_fp32)) != MOE_OK) return r;
+    if ((r = check_estride(&dw_estride, E, N, K, lddw, 1)) != MOE_OK) return r;
+    if (n_rows == 0) {   // no operand is read: any aligned address describes it
+        x = dy = reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(dw) & ~uintptr_t(15));
+        ldx = (int64_t)align_up(K, 8);
+        lddy = (int64_t)align_up(N, 8);
+    }
+    if ((r = check_operand("dy", dy, N, lddy, 2)) != MOE_OK) return r;
+    if ((r = check_operand("x", x, K, ldx, 2)) != MOE_OK) return r;
+    GemmArgs a{kGemmOpWgrad, E, N, K, n_rows, offsets, dy, lddy, x, ldx, 0, nullptr, nullptr, 0,
+               dw, lddw, dw_estride, dw_is_fp32, accumulate};
+    return launch_grouped_gemm(a, num_sms(current_device()), (cudaStream_t)stream);
+}
+
+moe_status moe_grouped_gemm_fp8(const void *xq, int64_t ldx, const float *xs, int n_rows, const int32_t *offsets,
+                                const void *wq, int64_t ldw, int64_t w_estride, const float *ws, int64_t ws_estride,
+                                int E, int N, int K, void *y, int64_t ldy, int y_is_fp32, moe_stream_t stream) {
+    moe_status r = check_product(E, N, K, n_rows, offsets);
+    if (r != MOE_OK || n_rows == 0) return r;
+    if ((r = check_operand("xq", xq, K, ldx, 1)) != MOE_OK) return r;
+    if ((r = check_operand("wq", wq, K, ldw, 1)) != MOE_OK) return r;
+    if ((r = check_estride(&w_estride, E, N, K, ldw, 16)) != MOE_OK) return r;
+    const int KB = (K + 127) / 128;
+    if ((r = check_estride(&ws_estride, E, N, KB, KB, 1)) != MOE_OK) return r;
+    if (!xs || !ws) return set_error(MOE_ERR_INVALID_ARG, "xs or ws is NULL");
+    if (misaligned(xs, 4) || misaligned(ws, 4)) return set_error(MOE_ERR_INVALID_ARG, "xs and ws must be 4-byte aligned");
+    if ((r = check_result(y, N, ldy, y_is_fp32)) != MOE_OK) return r;
+    GemmArgs a{kGemmOpFp8, E, N, K, n_rows, offsets, xq, ldx, wq, ldw, w_estride, xs, ws, ws_estride,
+               y, ldy, 0, y_is_fp32, 0};
+    return launch_grouped_gemm(a, num_sms(current_device()), (cudaStream_t)stream);
+}
+
+moe_status moe_quantize_fp8(const void *x, int64_t ldx, int rows, int K, int swiglu, void *codes, int64_t ldc,
+                            float *scale, moe_stream_t stream) {
+    if (rows < 0 || K <= 0 || K % 16 || K > kMaxProductDim)
+        return set_error(MOE_ERR_INVALID_ARG, "rows=%d < 0 or K=%d not a positive multiple of 16", rows, K);
+    if (rows == 0) return MOE_OK;
+    if (!x || !codes || !scale) return set_error(MOE_ERR_INVALID_ARG, "NULL pointer");
+    const int64_t width = swiglu ? 2 * (int64_t)K : K;
+    if (ldx < width || ldx % 8 || ldc < K || ldc % 8)
+        return set_error(MOE_ERR_INVALID_ARG, "ldx=%lld and ldc=%lld must hold a row and be multiples of 8",
+                         (long long)ldx, (long long)ldc);
+    if (misaligned(x, 16) || misaligned(codes, 8) || misaligned(scale, 4))
+        return set_error(MOE_ERR_INVALID_ARG, "x must be 16-byte aligned, codes 8-byte aligned, scale 4-byte aligned");
+    return launch_quantize_fp8(x, ldx, rows, K, swiglu, codes, ldc, scale, num_sms(current_device()),
+                               (cudaStream_t)stream);
 }
 
 moe_status moe_dequantize(int fmt, const void *w, const void *scale, float tscale, int rows, int K, void *out,

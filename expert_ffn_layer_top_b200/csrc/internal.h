@@ -186,6 +186,25 @@ moe_status launch_combine(const void *y_perm, int y_is_fp32, const int32_t *pair
 moe_status make_tmap(CUtensorMap *m, CUtensorMapDataType dt, int rank, const void *base, const uint64_t *dims,
                      const uint64_t *strides_bytes, const uint32_t *box, CUtensorMapSwizzle sw);
 
+// products grouped by expert and the FP8 quantiser (gemm.cu); strides in elements
+enum { kGemmOpForward = 0, kGemmOpDgrad = 1, kGemmOpWgrad = 2, kGemmOpFp8 = 3 };
+struct GemmArgs {
+    int op, E, N, K, n_rows;
+    const int32_t *offsets;      // [E+1]; null: one expert with all rows
+    const void *x;               // forward, fp8: x; dgrad, wgrad: dy
+    int64_t ldx;
+    const void *w;               // weights [E][N][K]; wgrad: x
+    int64_t ldw, w_estride;
+    const float *xs, *ws;        // fp8 scales, [n_rows][ceil(K/128)] and [E][N][ceil(K/128)]
+    int64_t ws_estride;
+    void *out;
+    int64_t ldo, out_estride;    // out_estride: wgrad
+    int out_fp32, accumulate;
+};
+moe_status launch_grouped_gemm(const GemmArgs &a, int nsm, cudaStream_t st);
+moe_status launch_quantize_fp8(const void *x, int64_t ldx, int rows, int K, int swiglu, void *codes, int64_t ldc,
+                               float *scale, int nsm, cudaStream_t st);
+
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 }  // namespace moe

@@ -7,5 +7,6 @@
 #include "ffn_tc.cu"
 #include "ffn_mx.cu"
 #include "prepack.cu"
+#include "gemm.cu"
 #include "cache.cu"
 #include "peak.cu"

@@ -254,6 +254,90 @@ moe_status moe_combine(const void *y_perm, int y_is_fp32, const int32_t *pair_ro
 moe_status moe_dequantize(int fmt, const void *w, const void *scale, float tscale, int rows, int K, void *out,
                           moe_stream_t stream);
 
+/* ------------------------------------------------- products grouped by expert */
+/* The expert products by themselves, and their gradients, for callers that put
+ * something else between them than the SwiGLU of moe_grouped_ffn, that train
+ * the experts, or that run FP8 experts on FP8 activations. The pages have no
+ * counterpart: they name the expert formats ([P4] "Reported Numbers and
+ * Ecosystem Position") and no product.
+ *
+ * For all of them:
+ *   - Rows are (token, expert) pairs in expert order, columns in natural order
+ *     (moe_permute with af = MOE_ACT_A4 writes such rows): expert e has the rows
+ *     offsets[e] .. offsets[e+1]-1. offsets is int32 [E+1] on the device, as
+ *     moe_permute writes it; NULL with E = 1 means all n_rows rows (a plain
+ *     matrix product). offsets[0] may be above 0 and offsets[E] below n_rows:
+ *     rows outside the experts' ranges are neither read into a result nor
+ *     written. Offsets outside 0..n_rows or decreasing ones are found on the
+ *     device: they are cut to 0..n_rows (an expert whose end is not above its
+ *     start has no rows) and the device error word is set to 2.
+ *   - Experts may be without rows. A value of one row never enters another
+ *     row's result, nor that of another expert, infinities and NaN included.
+ *   - ld* are the elements from one row to the next, *_estride those from one
+ *     expert to the next (0 = dense, N * ld). Operands: base 16-byte aligned,
+ *     strides multiples of 16 bytes. Results: aligned to their elements, any
+ *     stride that holds a row; 16-byte aligned ones are stored faster. A result
+ *     must not overlap an operand.
+ *   - Sums are kept in fp32 and rounded once, to bf16 or not at all. The order
+ *     of a row's sum depends on the sizes only, so equal calls give equal bits.
+ *   - E in 1..1024; N, K >= 1, without further multiples beyond the strides'.
+ *     n_rows == 0 is a no-op (wgrad: dw is cleared, or kept with accumulate).
+ *   - No workspace and no synchronisation; calls can be captured into graphs.
+ *   Errors: UNSUPPORTED for E outside 1..1024, N or K above 2^24 or n_rows above
+ *   2^30; INVALID_ARG for N, K or n_rows below their range, NULL pointers,
+ *   misaligned ones, or strides that break the rules above. */
+
+/* y[r][n] = sum_k x[r][k] w[e][n][k].
+ *   x: bf16 [n_rows][K]; w: bf16 [E][N][K]; y: [n_rows][N], bf16, or fp32 if y_is_fp32. */
+moe_status moe_grouped_gemm(const void *x, int64_t ldx, int n_rows, const int32_t *offsets, const void *w,
+                            int64_t ldw, int64_t w_estride, int E, int N, int K, void *y, int64_t ldy, int y_is_fp32,
+                            moe_stream_t stream);
+
+/* The gradient of moe_grouped_gemm for x: dx[r][k] = sum_n dy[r][n] w[e][n][k].
+ *   dy: bf16 [n_rows][N]; w: bf16 [E][N][K] as in the forward product (no
+ *   transposed copy is needed); dx: [n_rows][K], bf16, or fp32 if dx_is_fp32. */
+moe_status moe_grouped_gemm_dgrad(const void *dy, int64_t lddy, int n_rows, const int32_t *offsets, const void *w,
+                                  int64_t ldw, int64_t w_estride, int E, int N, int K, void *dx, int64_t lddx,
+                                  int dx_is_fp32, moe_stream_t stream);
+
+/* The gradient for w: dw[e][n][k] = sum over e's rows of dy[r][n] x[r][k], 0 for
+ * an expert without rows.
+ *   dy: bf16 [n_rows][N]; x: bf16 [n_rows][K]; dw: [E][N][K], fp32 if dw_is_fp32,
+ *   else bf16. accumulate: add to what dw holds, in fp32 (UNSUPPORTED for bf16);
+ *   an expert without rows then keeps its values. */
+moe_status moe_grouped_gemm_wgrad(const void *dy, int64_t lddy, const void *x, int64_t ldx, int n_rows,
+                                  const int32_t *offsets, int E, int N, int K, void *dw, int64_t lddw,
+                                  int64_t dw_estride, int dw_is_fp32, int accumulate, moe_stream_t stream);
+
+/* Activations into the FP8 expert format: per row and 128-wide block of K (the
+ * last one may be shorter) s = amax / 448, or 1 where amax is 0, and codes
+ * E4M3(v / s), to nearest, ties to even, saturating; each step is one correctly
+ * rounded fp32 operation. A block that holds an infinity or a NaN decodes to NaN
+ * throughout.
+ *   swiglu 0: v = x[r][k], x bf16 [rows][K].
+ *   swiglu 1: v = silu(x[r][k]) * x[r][K + k] in fp32, x bf16 [rows][2K], the
+ *     rows that moe_grouped_gemm(_fp8) makes with w13 (gate, then up).
+ *   codes: E4M3 bytes [rows][K], ldc bytes a row; scale: fp32 [rows][ceil(K/128)],
+ *   dense. moe_dequantize(MOE_FP8_E4M3_K128) reads dense results back (K % 128 == 0,
+ *   finite blocks, scales below 128).
+ *   Requires K % 16 == 0, ldx % 8 == 0, ldc % 8 == 0 (moe_grouped_gemm_fp8: 16).
+ *   rows == 0 is a no-op. Errors: INVALID_ARG for sizes, strides or alignment
+ *   outside these (x 16, codes 8, scale 4 bytes) or NULL pointers. */
+moe_status moe_quantize_fp8(const void *x, int64_t ldx, int rows, int K, int swiglu, void *codes, int64_t ldc,
+                            float *scale, moe_stream_t stream);
+
+/* The forward product of E4M3 operands with fp32 scales per 128 of K on both
+ * sides, b running over the blocks (the last one may be shorter):
+ *   y[r][n] = sum_b (sum_{k in b} xq[r][k] wq[e][n][k]) * xs[r][b] * ws[e][n][b].
+ *   xq, xs: as moe_quantize_fp8 writes them; wq: E4M3 [E][N][K]; ws: fp32
+ *   [E][N][ceil(K/128)], the MOE_FP8_E4M3_K128 experts' arrays in the STANDARD
+ *   layout. ldx, ldw, w_estride in bytes; ws_estride in floats (0 = dense).
+ *   Each block's sum is formed by the tensor core and added in fp32, with its
+ *   scales, to the running sum. y: bf16, or fp32 if y_is_fp32. */
+moe_status moe_grouped_gemm_fp8(const void *xq, int64_t ldx, const float *xs, int n_rows, const int32_t *offsets,
+                                const void *wq, int64_t ldw, int64_t w_estride, const float *ws, int64_t ws_estride,
+                                int E, int N, int K, void *y, int64_t ldy, int y_is_fp32, moe_stream_t stream);
+
 /* Bytes of one expert's prepacked w13 (which = 0) or w2 (which = 1): equal to
  * its standard layout's code and scale bytes, since prepacking only reorders
  * bytes. Host-only; 0 for an unknown format, H or I not a positive multiple of
