@@ -1,7 +1,6 @@
 """ctypes binding of libmoe.so. Argument marshalling only (see include/moe.h)."""
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import os
 import threading
@@ -320,19 +319,31 @@ def moe_dequantize(fmt: str, w: torch.Tensor, scale: Optional[torch.Tensor], tsc
 _FP8 = (torch.uint8, torch.float8_e4m3fn)
 
 
-def _on(*ts: Optional[torch.Tensor]):
-    """The tensors' device, made current while the library is called."""
-    _need_cuda(*ts)
-    dev = next(t.device for t in ts if t is not None)
-    if any(t is not None and t.device != dev for t in ts):
-        raise ValueError("tensors on one device expected")
-    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else contextlib.nullcontext()
+def _device(*ts: Optional[torch.Tensor]) -> int:
+    """Index of the one CUDA device that the tensors are on."""
+    d = ts[0].get_device()
+    if d < 0:
+        raise ValueError("device tensors expected")
+    for t in ts:
+        if t is not None and t.get_device() != d:
+            raise ValueError("tensors on one device expected")
+    return d
+
+
+def _run(d: int, fn, *args):
+    """Call fn(*args, stream) on device d and its current stream."""
+    if d != torch._C._cuda_getDevice():
+        with torch.cuda.device(d):
+            return _check(fn(*args, torch._C._cuda_getCurrentRawStream(d)))
+    status = fn(*args, torch._C._cuda_getCurrentRawStream(d))
+    if status:
+        _check(status)
 
 
 def _matrix(name: str, t: torch.Tensor, dtypes, ndim: int = 2):
     if t.dtype not in dtypes or t.dim() != ndim:
         raise ValueError(f"{name}: expected {ndim}-D {' or '.join(str(d) for d in dtypes)}, got {t.dim()}-D {t.dtype}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
 
 
@@ -342,25 +353,30 @@ def _ld(t: torch.Tensor) -> int:
 
 
 def _estride(t: torch.Tensor) -> int:
-    if t.shape[0] > 1 and t.stride(0) == 0:   # 0 means dense in the C ABI
+    if t.shape[0] <= 1:
+        return 0
+    if t.stride(0) == 0:   # 0 means dense in the C ABI
         raise ValueError("experts expanded from one: pass a copy per expert")
-    return t.stride(0) if t.shape[0] > 1 else 0
+    return t.stride(0)
 
 
 def _offsets(offsets: Optional[torch.Tensor], E: int):
+    """Address of the offsets of E experts (None: one expert has all rows)."""
     if offsets is None:
         if E != 1:
             raise ValueError("offsets: needed with more than one expert")
-    elif offsets.dtype != torch.int32 or offsets.shape != (E + 1,) or not offsets.is_contiguous():
+        return None
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] != E + 1 or not offsets.is_contiguous():
         raise ValueError(f"offsets: expected contiguous int32 [{E + 1}]")
+    return offsets.data_ptr()
 
 
 def _result(out: Optional[torch.Tensor], shape, fp32: bool, device) -> torch.Tensor:
     dtype = torch.float32 if fp32 else torch.bfloat16
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"out: expected shape {tuple(shape)}, got {tuple(out.shape)}")
+    if tuple(out.shape) != shape:
+        raise ValueError(f"out: expected shape {shape}, got {tuple(out.shape)}")
     _matrix("out", out, (dtype,), len(shape))
     return out
 
@@ -369,20 +385,24 @@ def _experts_of(w: torch.Tensor) -> torch.Tensor:
     return w.unsqueeze(0) if w.dim() == 2 else w
 
 
+_BF16 = (torch.bfloat16,)
+
+
 def moe_grouped_gemm(x: torch.Tensor, offsets: Optional[torch.Tensor], w: torch.Tensor, y_fp32: bool = False,
                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y[r] = w[e] x[r] for the rows r of expert e; w bf16 [E, N, K] (or [N, K] with offsets None)."""
     w = _experts_of(w)
-    _matrix("x", x, (torch.bfloat16,))
-    _matrix("w", w, (torch.bfloat16,), 3)
+    _matrix("x", x, _BF16)
+    _matrix("w", w, _BF16, 3)
     E, N, K = w.shape
+    rows = x.shape[0]
     if x.shape[1] != K:
         raise ValueError(f"x has {x.shape[1]} columns, w {K}")
-    _offsets(offsets, E)
-    with _on(x, offsets, w, out):
-        y = _result(out, (x.shape[0], N), y_fp32, x.device)
-        _check(lib().moe_grouped_gemm(_ptr(x), _ld(x), x.shape[0], _ptr(offsets), _ptr(w), _ld(w), _estride(w), E, N, K,
-                                      _ptr(y), _ld(y), int(y_fp32), _stream()))
+    off = _offsets(offsets, E)
+    d = _device(x, offsets, w, out)
+    y = _result(out, (rows, N), y_fp32, x.device)
+    _run(d, lib().moe_grouped_gemm, x.data_ptr(), _ld(x), rows, off, w.data_ptr(), _ld(w), _estride(w), E, N, K,
+         y.data_ptr(), _ld(y), int(y_fp32))
     return y
 
 
@@ -390,16 +410,17 @@ def moe_grouped_gemm_dgrad(dy: torch.Tensor, offsets: Optional[torch.Tensor], w:
                            out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dx[r] = w[e]^T dy[r]: the gradient of moe_grouped_gemm for x."""
     w = _experts_of(w)
-    _matrix("dy", dy, (torch.bfloat16,))
-    _matrix("w", w, (torch.bfloat16,), 3)
+    _matrix("dy", dy, _BF16)
+    _matrix("w", w, _BF16, 3)
     E, N, K = w.shape
+    rows = dy.shape[0]
     if dy.shape[1] != N:
         raise ValueError(f"dy has {dy.shape[1]} columns, w {N} rows")
-    _offsets(offsets, E)
-    with _on(dy, offsets, w, out):
-        dx = _result(out, (dy.shape[0], K), dx_fp32, dy.device)
-        _check(lib().moe_grouped_gemm_dgrad(_ptr(dy), _ld(dy), dy.shape[0], _ptr(offsets), _ptr(w), _ld(w), _estride(w),
-                                            E, N, K, _ptr(dx), _ld(dx), int(dx_fp32), _stream()))
+    off = _offsets(offsets, E)
+    d = _device(dy, offsets, w, out)
+    dx = _result(out, (rows, K), dx_fp32, dy.device)
+    _run(d, lib().moe_grouped_gemm_dgrad, dy.data_ptr(), _ld(dy), rows, off, w.data_ptr(), _ld(w), _estride(w), E, N, K,
+         dx.data_ptr(), _ld(dx), int(dx_fp32))
     return dx
 
 
@@ -407,33 +428,37 @@ def moe_grouped_gemm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: Optional[
                            out: Optional[torch.Tensor] = None, accumulate: bool = False) -> torch.Tensor:
     """dw[e] = sum of dy[r] x[r]^T over the rows of expert e: the gradient of moe_grouped_gemm for w
     ([E, N, K]; E = 1 with offsets None). accumulate adds to `out`."""
-    _matrix("dy", dy, (torch.bfloat16,))
-    _matrix("x", x, (torch.bfloat16,))
-    if x.shape[0] != dy.shape[0]:
-        raise ValueError(f"dy has {dy.shape[0]} rows, x {x.shape[0]}")
+    _matrix("dy", dy, _BF16)
+    _matrix("x", x, _BF16)
+    rows = x.shape[0]
+    if rows != dy.shape[0]:
+        raise ValueError(f"dy has {dy.shape[0]} rows, x {rows}")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    E = 1 if offsets is None else offsets.numel() - 1
+    E = 1 if offsets is None else max(offsets.numel() - 1, 0)
     N, K = dy.shape[1], x.shape[1]
-    _offsets(offsets, E)
-    with _on(dy, x, offsets, out):
-        dw = _result(out, (E, N, K), dw_fp32, x.device)
-        _check(lib().moe_grouped_gemm_wgrad(_ptr(dy), _ld(dy), _ptr(x), _ld(x), x.shape[0], _ptr(offsets), E, N, K,
-                                            _ptr(dw), _ld(dw), _estride(dw), int(dw_fp32), int(accumulate), _stream()))
+    off = _offsets(offsets, E)
+    d = _device(dy, x, offsets, out)
+    dw = _result(out, (E, N, K), dw_fp32, x.device)
+    _run(d, lib().moe_grouped_gemm_wgrad, dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), rows, off, E, N, K,
+         dw.data_ptr(), _ld(dw), _estride(dw), int(dw_fp32), int(accumulate))
     return dw
 
 
 def moe_quantize_fp8(x: torch.Tensor, swiglu: bool = False):
     """(E4M3 codes uint8 [rows, K], fp32 scales [rows, ceil(K/128)]) of bf16 rows x [rows, K], or of
     silu(gate) * up of x [rows, 2K] with swiglu."""
-    _matrix("x", x, (torch.bfloat16,))
-    if swiglu and x.shape[1] % 2:
-        raise ValueError("x: gate and up halves expected")
-    rows, K = x.shape[0], x.shape[1] // 2 if swiglu else x.shape[1]
-    with _on(x):
-        codes = torch.empty(rows, K, dtype=torch.uint8, device=x.device)
-        scale = torch.empty(rows, -(-K // 128), dtype=torch.float32, device=x.device)
-        _check(lib().moe_quantize_fp8(_ptr(x), _ld(x), rows, K, int(swiglu), _ptr(codes), K, _ptr(scale), _stream()))
+    _matrix("x", x, _BF16)
+    rows, K = x.shape
+    if swiglu:
+        if K % 2:
+            raise ValueError("x: gate and up halves expected")
+        K //= 2
+    d = _device(x)
+    device = x.device
+    codes = torch.empty((rows, K), dtype=torch.uint8, device=device)
+    scale = torch.empty((rows, -(-K // 128)), dtype=torch.float32, device=device)
+    _run(d, lib().moe_quantize_fp8, x.data_ptr(), _ld(x), rows, K, int(swiglu), codes.data_ptr(), K, scale.data_ptr())
     return codes, scale
 
 
@@ -446,18 +471,18 @@ def moe_grouped_gemm_fp8(xq: torch.Tensor, xs: torch.Tensor, offsets: Optional[t
     _matrix("wq", wq, _FP8, 3)
     E, N, K = wq.shape
     KB = -(-K // 128)
+    rows = xq.shape[0]
     if xq.shape[1] != K:
         raise ValueError(f"xq has {xq.shape[1]} columns, wq {K}")
-    if xs.dtype != torch.float32 or xs.shape != (xq.shape[0], KB) or not xs.is_contiguous():
-        raise ValueError(f"xs: expected contiguous float32 [{xq.shape[0]}, {KB}]")
-    if ws.dtype != torch.float32 or ws.shape != (E, N, KB) or (E > 0 and not ws[0].is_contiguous()):
+    if xs.dtype != torch.float32 or tuple(xs.shape) != (rows, KB) or not xs.is_contiguous():
+        raise ValueError(f"xs: expected contiguous float32 [{rows}, {KB}]")
+    if ws.dtype != torch.float32 or tuple(ws.shape) != (E, N, KB) or (E > 0 and not ws[0].is_contiguous()):
         raise ValueError(f"ws: expected float32 [{E}, {N}, {KB}], dense per expert")
-    _offsets(offsets, E)
-    with _on(xq, xs, offsets, wq, ws, out):
-        y = _result(out, (xq.shape[0], N), y_fp32, xq.device)
-        _check(lib().moe_grouped_gemm_fp8(_ptr(xq), _ld(xq), _ptr(xs), xq.shape[0], _ptr(offsets), _ptr(wq), _ld(wq),
-                                          _estride(wq), _ptr(ws), _estride(ws), E, N, K, _ptr(y), _ld(y), int(y_fp32),
-                                          _stream()))
+    off = _offsets(offsets, E)
+    d = _device(xq, xs, offsets, wq, ws, out)
+    y = _result(out, (rows, N), y_fp32, xq.device)
+    _run(d, lib().moe_grouped_gemm_fp8, xq.data_ptr(), _ld(xq), xs.data_ptr(), rows, off, wq.data_ptr(), _ld(wq),
+         _estride(wq), ws.data_ptr(), _estride(ws), E, N, K, y.data_ptr(), _ld(y), int(y_fp32))
     return y
 
 

@@ -754,11 +754,11 @@ moe_status moe_quantize_fp8(const void *x, int64_t ldx, int rows, int K, int swi
     if (rows == 0) return MOE_OK;
     if (!x || !codes || !scale) return set_error(MOE_ERR_INVALID_ARG, "NULL pointer");
     const int64_t width = swiglu ? 2 * (int64_t)K : K;
-    if (ldx < width || ldx % 8 || ldc < K || ldc % 8)
-        return set_error(MOE_ERR_INVALID_ARG, "ldx=%lld and ldc=%lld must hold a row and be multiples of 8",
+    if (ldx < width || ldx % 8 || ldc < K || ldc % 16)
+        return set_error(MOE_ERR_INVALID_ARG, "ldx=%lld and ldc=%lld must hold a row and be multiples of 8 and 16",
                          (long long)ldx, (long long)ldc);
-    if (misaligned(x, 16) || misaligned(codes, 8) || misaligned(scale, 4))
-        return set_error(MOE_ERR_INVALID_ARG, "x must be 16-byte aligned, codes 8-byte aligned, scale 4-byte aligned");
+    if (misaligned(x, 16) || misaligned(codes, 16) || misaligned(scale, 4))
+        return set_error(MOE_ERR_INVALID_ARG, "x and codes must be 16-byte aligned, scale 4-byte aligned");
     return launch_quantize_fp8(x, ldx, rows, K, swiglu, codes, ldc, scale, num_sms(current_device()),
                                (cudaStream_t)stream);
 }

@@ -21,20 +21,23 @@
 #include "common.cuh"
 #include "internal.h"
 #include "mx_codec.cuh"
-#include <cstdlib>
+#include <type_traits>
 
 namespace moe {
 
 constexpr int kGemmFwd = 0, kGemmDgrad = 1, kGemmWgrad = 2, kGemmFp8 = 3;
 
-// Warps 0-3: TMA, MMA, scales, tail rows; from 4 on the epilogue: 16 warps for tiles of 256
-// columns (64 sums per thread; with 8 warps and 128 sums the fp8 kernel spilled), 8 for small.
-__host__ __device__ constexpr int gemm_epi_warps(int BN) { return BN >= 256 ? 16 : 8; }
-__host__ __device__ constexpr int gemm_threads(int BN) { return 128 + 32 * gemm_epi_warps(BN); }
+// Warps 0-3: TMA, MMA, scales, tail rows; from 4 on the epilogue: 16 warps for large bf16 tiles
+// (it stores once per tile, and many warps hide each other's latencies), 12 for large fp8 ones
+// (their sums stay in registers from K block to K block; 8 or 16 warps took 6% and 50% longer),
+// 8 for small tiles.
+__host__ __device__ constexpr int gemm_epi_warps(bool fp8, int BN) { return BN <= 64 ? 8 : fp8 ? 12 : 16; }
+__host__ __device__ constexpr int gemm_threads(bool fp8, int BN) { return 128 + 32 * gemm_epi_warps(fp8, BN); }
 constexpr int kGemmABytes = 128 * 128;     // one CTA's A tile of a stage: 128 m x 128 bytes
-constexpr int kGemmBoxRows = 32;           // rows of B in a small TMA box (K-major B); a large one has 128
+constexpr int kGemmBoxRows = 32;           // rows of B in a small TMA box (K-major B)
+__host__ __device__ constexpr int gemm_big_box(int rows) { return rows > 128 ? 128 : rows; }   // ... in a large one
 constexpr int kGemmMaxStages = 10;
-constexpr int kGemmXsSlots = 8;            // ring of activation scales (fp8), one slot per K block
+constexpr int kGemmXsSlots = 2;            // ring of scales (fp8), four K blocks each
 
 struct GemmParams {
     const int32_t *offsets;   // [E+1]; null: one expert with all rows
@@ -48,6 +51,8 @@ struct GemmParams {
     void *out;
     int64_t ldo, out_estride; // elements; out_estride: wgrad
     int out_fp32, accumulate;
+    int quads;                // fp8: weight rows in the lane order that gives a thread four neighbours
+    int vec;                  // fp8: results may be stored four at a time
     const float *xs, *ws;     // fp8 scales: [n_rows][xs_ld], [E][M][ws_ld]
     int64_t xs_ld, ws_ld, ws_estride;
 };
@@ -59,8 +64,8 @@ struct GemmSmem {
     uint64_t tailpeer[kGemmMaxStages];   // and the pair's other CTA has cleared its own
     uint64_t accfull[2], accempty[2];
     uint64_t scfull[kGemmXsSlots], scempty[kGemmXsSlots];
-    float xs[kGemmXsSlots][256];   // fp8: a K block's scales of the tile's rows and of this CTA's 128 weight rows
-    float ws[kGemmXsSlots][128];
+    float xs[kGemmXsSlots][4][256];   // fp8: scales of the tile's rows and of this CTA's 128 weight rows
+    float ws[kGemmXsSlots][4][128];
     uint32_t tmem_base;
     int abort_flag;
     int total_items;
@@ -156,6 +161,12 @@ __device__ __forceinline__ void cluster_sync_all() {
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
+// ... by the warp's lane 0, without a branch.
+__device__ __forceinline__ void mbar_arrive_remote_lane0(uint32_t addr) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(addr),
+                 "r"(threadIdx.x & 31)
+                 : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
@@ -191,6 +202,13 @@ __device__ __forceinline__ bool gemm_wait(uint64_t *bar, uint32_t parity, volati
     }
 }
 
+// A whole warp's wait: one answer for all lanes (no divergence, and the same where some lanes
+// gave up).
+__device__ __forceinline__ bool gemm_wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, gemm_wait(bar, parity, abort_flag));
+}
+
 // TMA boxes into this CTA's shared memory; `bar` is a shared::cluster address, the pair
 // leader's barrier for CTA pairs.
 template <int CG>
@@ -221,6 +239,23 @@ __device__ __forceinline__ void gemm_tma_3d(void *dst, const CUtensorMap *m, uin
             "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
             " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
             "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+            : "memory");
+}
+
+// Groups of 32 rows, row 4 a + b of a group in place 8 b + a: dimensions (c, a, b, group, expert).
+template <int CG>
+__device__ __forceinline__ void gemm_tma_5d(void *dst, const CUtensorMap *m, uint32_t bar, int c0, int g, int e) {
+    if (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+            "l"(m), "r"(bar), "r"(c0), "r"(0), "r"(g), "r"(e)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+            "l"(m), "r"(bar), "r"(c0), "r"(0), "r"(g), "r"(e)
             : "memory");
 }
 
@@ -285,16 +320,13 @@ __device__ __forceinline__ void gemm_tmem_dealloc(uint32_t t, uint32_t cols) {
 }
 
 // Pairs of fp32 in one 64-bit register.
-__device__ __forceinline__ uint64_t pack2u(uint32_t lo, uint32_t hi) {
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
     uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
     return r;
 }
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) { return pack2u(__float_as_uint(lo), __float_as_uint(hi)); }
-__device__ __forceinline__ float half2of(uint64_t p, int hi) {
-    uint32_t lo, up;
-    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(up) : "l"(p));
-    return __uint_as_float(hi ? up : lo);
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     uint64_t r;
@@ -307,20 +339,23 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return r;
 }
 
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
+// 16 lanes x 32 columns of an accumulator in the layout of matrix fragments: register 2k + i of
+// thread T is lane T/4 + 8i, column 4k + T%4. (Loads of 32 such columns for two warps a quarter
+// take 1.15 times as long as with a lane per thread; the wider fragments of 16x256b, 1.7 times.)
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x128b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
 }
-
 // tcgen05.wait::ld that the loaded registers pass through, so that no use of them can be
 // scheduled before it.
 __device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
 
 // Shared-memory descriptor of an MN-major tile in the 128-byte swizzle: 64 elements of the
@@ -336,19 +371,103 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
     return d;
 }
 
+// One element of the result. The stores stay in program order (volatile), so that the compiler
+// does not hold many addresses and converted values at once and spill. STREAM: read by a later
+// kernel at most, first to leave L2.
+template <bool F32, bool STREAM = false>
+__device__ __forceinline__ void gemm_store(const GemmParams &p, int64_t at, float v, bool on) {
+    if (F32) {
+        float *d = reinterpret_cast<float *>(p.out) + at;
+        if (STREAM)
+            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.global.cs.f32 [%0], %1;\n\t}" ::"l"(d), "f"(v),
+                         "r"((uint32_t)on)
+                         : "memory");
+        else
+            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.global.f32 [%0], %1;\n\t}" ::"l"(d), "f"(v),
+                         "r"((uint32_t)on)
+                         : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b16 h;\n\tsetp.ne.u32 p, %2, 0;\n\tcvt.rn.bf16.f32 h, %1;\n\t"
+            "@p st.global.b16 [%0], h;\n\t}" ::"l"(reinterpret_cast<__nv_bfloat16 *>(p.out) + at),
+            "f"(v), "r"((uint32_t)on)
+            : "memory");
+    }
+}
+
+// Four neighbouring elements at an aligned address.
+template <bool F32>
+__device__ __forceinline__ void gemm_store4(const GemmParams &p, int64_t at, const float (&v)[4], bool on) {
+    if (F32)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t@p st.global.v4.f32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(
+                         reinterpret_cast<float *>(p.out) + at),
+                     "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "r"((uint32_t)on)
+                     : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b32 a, b;\n\tsetp.ne.u32 p, %5, 0;\n\tcvt.rn.bf16x2.f32 a, %2, %1;\n\t"
+            "cvt.rn.bf16x2.f32 b, %4, %3;\n\t@p st.global.v2.b32 [%0], {a, b};\n\t}" ::"l"(
+                reinterpret_cast<__nv_bfloat16 *>(p.out) + at),
+            "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "r"((uint32_t)on)
+            : "memory");
+}
+
+// Adds ACT units (16 columns each, 16 G apart) of an accumulator at TMEM address t to the sums.
+template <int NU, int ACT, int G>
+__device__ __forceinline__ void gemm_add_part(float (&acc)[NU][16], uint32_t t) {
+#pragma unroll
+    for (int i = 0; i < ACT; ++i) {
+        uint32_t v[16];
+        tmem_ld16(t + i * (16 * G), v);
+        tmem_wait_ld16(v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[i][j] += __uint_as_float(v[j]);
+    }
+}
+
+// fp8: adds ACT groups (32 columns each, 32 G apart) of an accumulator, times the columns' scales
+// xs and the four lanes' scales w (pairs of lanes 8 apart), to the sums. In the fragment layout a
+// thread needs a quarter of the columns' scales; with a lane's whole row per thread the copies
+// of them filled the path from shared memory (128 bytes a clock) for longer than the arithmetic
+// takes, two operations an element (384 clocks a block of 192 columns).
+template <int NG, int ACT, int G>
+__device__ __forceinline__ void gemm_add_scaled(float (&acc)[NG][2][16], uint32_t t, const float *xs, const uint64_t (&w)[2]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < ACT; ++i) {
+        uint32_t v[16];
+        tmem_ld_16x32(t + i * (32 * G), v);
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = xs[i * (32 * G) + 4 * k + (lane & 3)];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (h) tmem_ld_16x32(t + i * (32 * G) + (16u << 16), v);
+            tmem_wait_ld16(v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                uint64_t a = pack2(acc[i][h][2 * k], acc[i][h][2 * k + 1]);
+                a = fma2(mul2(pack2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), pack2(f[k], f[k])), w[h], a);
+                unpack2(a, acc[i][h][2 * k], acc[i][h][2 * k + 1]);
+            }
+        }
+    }
+}
+
 // ------------------------------------------------------------------ kernel
 
 template <int MODE, int CG, int BN>
-__global__ void __launch_bounds__(gemm_threads(BN), 1)
+__global__ void __launch_bounds__(gemm_threads(MODE == kGemmFp8, BN), 1)
 gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
-            const __grid_constant__ CUtensorMap bmap128, GemmParams p) {
+            const __grid_constant__ CUtensorMap bbig, GemmParams p) {
     constexpr bool FP8 = MODE == kGemmFp8;
     constexpr bool A_MN = MODE == kGemmDgrad || MODE == kGemmWgrad, B_MN = MODE == kGemmWgrad;
-    constexpr int EPI = gemm_epi_warps(BN);
+    constexpr int EPI = gemm_epi_warps(FP8, BN);
     constexpr int BROWS = BN / CG;                       // j's of B that this CTA holds
+    constexpr int BIG = gemm_big_box(BROWS);
     constexpr int STAGE = kGemmABytes + BROWS * 128;
     constexpr int CB = FP8 ? 128 : 64;                   // c's per stage
-    constexpr uint32_t TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
+    constexpr uint32_t TMEM_COLS = BN <= 64 ? 128 : 512;   // a power of two with room for two accumulators
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int ns = p.stages;
@@ -358,9 +477,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
     const uint32_t rank = CG == 2 ? cluster_rank() : 0;
     const int first = CG == 2 ? blockIdx.x / 2 : blockIdx.x, step = CG == 2 ? gridDim.x / 2 : gridDim.x;
 
-    pdl_wait();
+    // what needs none of the previous kernel's results comes before the wait for it
     if (threadIdx.x == 0) {
-        pdl_release();
         for (int s = 0; s < ns; ++s) {
             mbar_init(&sm.full[s], 1);
             mbar_init(&sm.empty[s], 1);
@@ -372,29 +490,30 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
             mbar_init(&sm.accempty[b], CG * EPI);
         }
         for (int s = 0; s < kGemmXsSlots; ++s) {
-            mbar_init(&sm.scfull[s], 64);
+            mbar_init(&sm.scfull[s], 2);
             mbar_init(&sm.scempty[s], EPI);
         }
         sm.abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&amap);
         tma_prefetch_desc(&bmap);
-        if (MODE != kGemmWgrad && BROWS >= 128) tma_prefetch_desc(&bmap128);
+        if (MODE != kGemmWgrad && BIG > kGemmBoxRows) tma_prefetch_desc(&bbig);
     }
     if (warp == 2) gemm_tmem_alloc<CG>(&sm.tmem_base, TMEM_COLS);
-    if (warp == 3) {
+    pdl_wait();
+    if (threadIdx.x == 0) pdl_release();
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+        int beg, n;
+        gemm_range(p, e, beg, n);
+        sm.range[e] = make_int2(beg, n);
+    }
+    __syncthreads();
+    if (warp == 3) {   // first row tile of each expert
         int run = 0;
         if (lane == 0) sm.tile_start[0] = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
             const int e = e0 + lane;
-            int nt = 0;
-            if (e < p.E) {
-                int beg, n;
-                gemm_range(p, e, beg, n);
-                sm.range[e] = make_int2(beg, n);
-                nt = (n + BN - 1) / BN;
-            }
-            int incl = nt;
+            int incl = e < p.E ? (sm.range[e].y + BN - 1) / BN : 0;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int v = __shfl_up_sync(0xffffffffu, incl, d);
@@ -421,14 +540,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
             for (int item = first; item < total && ok; item += step) {
                 const GemmItem it = gemm_item<MODE, CG, BN>(sm, p, item);
                 const int bj0 = it.j0 + (int)rank * (it.nt / CG);          // this CTA's share of B
-                // K-major B in boxes of 128 rows, a rest of up to 96 rows in boxes of 32: few boxes
+                // K-major B in boxes of BIG rows, a smaller rest in boxes of 32: few boxes
                 // when the tile is full (issuing 4 KB boxes only cost a quarter of the rate), no
                 // more than 31 rows too many when it is not
                 const int share = it.nt / CG;
-                const int big = BROWS < 128 ? 0 : (share + 31) / 128;
-                const int small = big * 128 >= share ? 0 : (share - big * 128 + kGemmBoxRows - 1) / kGemmBoxRows;
+                const int big = BIG > kGemmBoxRows ? (share + 31) / BIG : 0;
+                const int small = big * BIG >= share ? 0 : (share - big * BIG + kGemmBoxRows - 1) / kGemmBoxRows;
                 const int chunks = (share + 63) / 64;
-                const uint32_t bytes = kGemmABytes + (B_MN ? chunks * 8192 : big * 16384 + small * kGemmBoxRows * 128);
+                const uint32_t bytes = kGemmABytes + (B_MN ? chunks * 8192 : (big * BIG + small * kGemmBoxRows) * 128);
                 const int m0 = it.m0 + (int)rank * 128;
                 for (int kb = 0; kb < it.kblocks; ++kb) {
                     if (!gemm_wait(&sm.empty[s], ph ^ 1, abort_flag)) { ok = false; break; }
@@ -450,13 +569,15 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
                         if (A_MN) {
                             gemm_tma_3d<CG>(a, &amap, bar, m0, c0, it.e);
                             gemm_tma_3d<CG>(a + 8192, &amap, bar, m0 + 64, c0, it.e);
+                        } else if (FP8 && p.quads) {
+                            gemm_tma_5d<CG>(a, &amap, bar, c0, m0 / 32, it.e);
                         } else {
                             gemm_tma_3d<CG>(a, &amap, bar, c0, m0, it.e);
                         }
-                        for (int i = 0; i < big; ++i) gemm_tma_2d<CG>(b + i * 16384, &bmap128, bar, c0, bj0 + i * 128);
+                        for (int i = 0; i < big; ++i) gemm_tma_2d<CG>(b + i * BIG * 128, &bbig, bar, c0, bj0 + i * BIG);
                         for (int i = 0; i < small; ++i)
-                            gemm_tma_2d<CG>(b + big * 16384 + i * kGemmBoxRows * 128, &bmap, bar, c0,
-                                            bj0 + big * 128 + i * kGemmBoxRows);
+                            gemm_tma_2d<CG>(b + (big * BIG + i * kGemmBoxRows) * 128, &bmap, bar, c0,
+                                            bj0 + big * BIG + i * kGemmBoxRows);
                     }
                     ++kc;
                     if (++s == ns) { s = 0; ph ^= 1; }
@@ -472,15 +593,22 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
             }
         }
     } else if (warp == 1) {
-        // =================================================== MMA issuer (one thread of the leader)
-        if (lane == 0 && rank == 0) {
+        // =================================================== MMA issuer (the leader's)
+        // The whole warp runs the loop, so that descriptors and barrier addresses are uniform
+        // values, and one elected thread issues: with the loop inside that thread each block
+        // took some 400 cycles to issue, more than its MMAs take to run.
+        if (rank == 0) {
             constexpr uint32_t idesc0 = (1u << 4) | (FP8 ? 0u : (1u << 7) | (1u << 10)) | (A_MN ? 1u << 15 : 0u) |
                                         (B_MN ? 1u << 16 : 0u) | ((uint32_t)(128 * CG >> 4) << 24);
-            int s = 0, u = 0;   // u: accumulator uses so far
+            constexpr uint64_t AK = A_MN ? 128 : 2, BK = B_MN ? 128 : 2;   // 16 (fp8: 32) c's further
+            const bool issues = elect_one();
             const int part = FP8 ? 1 : p.part;
+            const uint32_t ring0 = smem_u32(ring);
+            const uint64_t ad0 = A_MN ? smem_desc_mn_sw128(ring0) : smem_desc_sw128(ring0);
+            const uint64_t bd0 = B_MN ? smem_desc_mn_sw128(ring0 + kGemmABytes) : smem_desc_sw128(ring0 + kGemmABytes);
+            int s = 0, u = 0;   // u: accumulator uses so far
             uint32_t ph = 0;
             bool ok = true;
-            const uint32_t ring0 = smem_u32(ring);
             for (int item = first; item < total && ok; item += step) {
                 const GemmItem it = gemm_item<MODE, CG, BN>(sm, p, item);
                 const uint32_t idesc = idesc0 | ((uint32_t)(it.nt >> 3) << 17);
@@ -489,56 +617,88 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
                     const bool fresh = left == 0;
                     if (fresh) {
                         left = min(part, it.kblocks - kb);
-                        if (!gemm_wait(&sm.accempty[u & 1], ((u >> 1) & 1) ^ 1, abort_flag)) { ok = false; break; }
+                        if (!gemm_wait_warp(&sm.accempty[u & 1], ((u >> 1) & 1) ^ 1, abort_flag)) { ok = false; break; }
                     }
-                    const uint32_t d = tmem + (u & 1) * BN;
-                    if (!gemm_wait(&sm.full[s], ph, abort_flag)) { ok = false; break; }
+                    if (!gemm_wait_warp(&sm.full[s], ph, abort_flag)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t sa = ring0 + s * STAGE, sb = sa + kGemmABytes;
-                    const uint64_t ad = A_MN ? smem_desc_mn_sw128(sa) : smem_desc_sw128(sa);
-                    const uint64_t bd = B_MN ? smem_desc_mn_sw128(sb) : smem_desc_sw128(sb);
-                    int steps = 4;
-                    if (MODE == kGemmWgrad) steps = min(4, (it.valid - kb * 64 + 15) / 16);
-                    for (int i = 0; i < steps; ++i)   // 16 (fp8: 32) c's each
-                        gemm_mma<CG, FP8>(d, ad + (A_MN ? 128 : 2) * i, bd + (B_MN ? 128 : 2) * i, idesc,
-                                          !(fresh && i == 0));
-                    gemm_commit<CG>(&sm.empty[s]);
-                    if (--left == 0) {
-                        gemm_commit<CG>(&sm.accfull[u & 1]);
-                        ++u;
+                    const uint32_t d = tmem + (u & 1) * BN;
+                    const uint64_t ad = ad0 + (uint32_t)(s * (STAGE / 16)), bd = bd0 + (uint32_t)(s * (STAGE / 16));
+                    const bool last = --left == 0;
+                    if (issues) {
+                        if (MODE == kGemmWgrad && it.valid - kb * 64 < 49) {   // the steps with rows of the expert
+                            for (int i = 0; i < (it.valid - kb * 64 + 15) / 16; ++i)
+                                gemm_mma<CG, FP8>(d, ad + AK * i, bd + BK * i, idesc, !(fresh && i == 0));
+                        } else {
+                            gemm_mma<CG, FP8>(d, ad, bd, idesc, !fresh);
+                            gemm_mma<CG, FP8>(d, ad + AK, bd + BK, idesc, 1);
+                            gemm_mma<CG, FP8>(d, ad + 2 * AK, bd + 2 * BK, idesc, 1);
+                            gemm_mma<CG, FP8>(d, ad + 3 * AK, bd + 3 * BK, idesc, 1);
+                        }
+                        gemm_commit<CG>(&sm.empty[s]);
+                        if (last) gemm_commit<CG>(&sm.accfull[u & 1]);
                     }
+                    __syncwarp();
+                    if (last) ++u;
                     if (++s == ns) { s = 0; ph ^= 1; }
                 }
             }
         }
     } else if (FP8 && (warp == 2 || warp == 3)) {
         // =================================================== scales (fp8)
-        // A K block's scales of the tile's rows and of the CTA's 128 weight rows, copied
-        // asynchronously so that the whole ring of slots is in flight.
+        // The scales of the tile's rows and of the CTA's 128 weight rows, four K blocks at a time
+        // (one 16-byte load a row where the arrays allow it: a 4-byte copy a row and block kept
+        // the L1 busy for longer than the block's MMAs), transposed on the way into the slots of
+        // four. The next four are loaded before this warp waits for a slot.
         constexpr int R = (BN + 128 + 63) / 64;   // per lane of the two warps, counting rows of x, then of w
-        int x = 0;   // K blocks so far
+        const bool vec = p.xs_ld % 4 == 0 && p.ws_estride % 4 == 0 &&
+                         ((reinterpret_cast<uintptr_t>(p.xs) | reinterpret_cast<uintptr_t>(p.ws)) & 15) == 0;
+        int x = 0;   // slots filled so far
         bool ok = true;
         for (int item = first; item < total && ok; item += step) {
             const GemmItem it = gemm_item<MODE, CG, BN>(sm, p, item);
-            const int mbase = it.m0 + (int)rank * 128;
-            for (int kb = 0; kb < it.kblocks; ++kb, ++x) {
-                const int slot = x % kGemmXsSlots;
-                if (!gemm_wait(&sm.scempty[slot], ((x / kGemmXsSlots) & 1) ^ 1, abort_flag)) { ok = false; break; }
+            const int r0 = (warp - 2) * 32 + lane, mbase = it.m0 + (int)rank * 128;
+            float4 nx[R];
+            auto load = [&](int kb) {
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
-                    const int r = (warp - 2) * 32 + lane + 64 * i, w = r - BN;
-                    if (w >= 128) continue;
-                    const bool on = w < 0 ? r < it.valid : mbase + w < p.M;
+                    const int r = r0 + 64 * i, w = r - BN;
+                    nx[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (!(w < 0 ? r < it.valid : w < 128 && mbase + w < p.M) || kb >= it.kblocks) continue;
                     const float *src = w < 0 ? p.xs + (int64_t)(it.row0 + r) * p.xs_ld + kb
                                              : p.ws + (int64_t)it.e * p.ws_estride + (int64_t)(mbase + w) * p.ws_ld + kb;
-                    const uint32_t dst = smem_u32(w < 0 ? &sm.xs[slot][r] : &sm.ws[slot][w]);
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(on ? src : p.xs), "r"(on ? 4 : 0)
-                                 : "memory");
+                    if (vec) {
+                        nx[i] = __ldg(reinterpret_cast<const float4 *>(src));
+                    } else {
+                        nx[i].x = src[0];
+                        if (kb + 1 < it.kblocks) nx[i].y = src[1];
+                        if (kb + 2 < it.kblocks) nx[i].z = src[2];
+                        if (kb + 3 < it.kblocks) nx[i].w = src[3];
+                    }
                 }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sm.scfull[slot])) : "memory");
+            };
+            load(0);
+            for (int kb = 0; kb < it.kblocks && ok; kb += 4) {
+                float4 cur[R];
+#pragma unroll
+                for (int i = 0; i < R; ++i) cur[i] = nx[i];
+                load(kb + 4);
+                const int slot = x % kGemmXsSlots;
+                if (!gemm_wait_warp(&sm.scempty[slot], ((x / kGemmXsSlots) & 1) ^ 1, abort_flag)) { ok = false; break; }
+                ++x;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        const int r = r0 + 64 * i, w = r - BN;
+                        const float v = b == 0 ? cur[i].x : b == 1 ? cur[i].y : b == 2 ? cur[i].z : cur[i].w;
+                        if (w < 0) sm.xs[slot][b][r] = v;
+                        else if (w < 128) sm.ws[slot][b][w] = v;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.scfull[slot]);
             }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp < 4) {
         // =================================================== wgrad (warp 3): rows behind the expert's last
         // The last block of an expert holds rows of the next one; the up to 15 of them that
@@ -552,7 +712,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
                 if (!it.kblocks) continue;
                 s = (s + it.kblocks - 1) % ns;   // the stage of the last block
                 if (it.valid & 15) {
-                    if (!gemm_wait(&sm.tail[s], (tph >> s) & 1, abort_flag)) { ok = false; break; }
+                    if (!gemm_wait_warp(&sm.tail[s], (tph >> s) & 1, abort_flag)) { ok = false; break; }
                     tph ^= 1u << s;
                     uint8_t *a = ring + s * STAGE;
                     const int r0 = it.valid & 63, r1 = (r0 + 15) & ~15;
@@ -566,7 +726,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
                     if (CG == 2 && rank == 1) {
                         if (lane == 0) mbar_arrive_cluster(mapa_u32(smem_u32(&sm.tailpeer[s]), 0));
                     } else {
-                        if (CG == 2 && !gemm_wait<true>(&sm.tailpeer[s], ((tph >> s) & 1) ^ 1, abort_flag)) { ok = false; break; }
+                        if (CG == 2 && !__all_sync(0xffffffffu, gemm_wait<true>(&sm.tailpeer[s], ((tph >> s) & 1) ^ 1, abort_flag))) { ok = false; break; }
                         if (lane == 0) mbar_arrive(&sm.full[s]);
                     }
                 }
@@ -575,106 +735,117 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
         }
     } else {
         // =================================================== epilogue
-        // Warp quarter q owns TMEM lanes 32q..32q+31; the quarter's G warps take turns on units
-        // of 16 columns.
+        // Warp quarter q owns TMEM lanes 32q..32q+31; the quarter's G warps take turns on groups
+        // of columns.
         constexpr int G = EPI / 4;
         const int q = warp & 3, g = (warp - 4) >> 2;
         const uint32_t lead_empty0 = CG == 2 ? mapa_u32(smem_u32(&sm.accempty[0]), 0) : smem_u32(&sm.accempty[0]);
-        constexpr int NU = BN / (16 * G);   // units per warp
-        const int part = FP8 ? 1 : p.part;
-        int u = 0;
+        int u = 0;   // accumulators used so far
         bool ok = true;
-        for (int item = first; item < total && ok; item += step) {
-            const GemmItem it = gemm_item<MODE, CG, BN>(sm, p, item);
-            const int m = it.m0 + (int)rank * 128 + q * 32 + lane;
-            const bool mok = m < p.M;
-            const int jn = MODE == kGemmWgrad ? min(it.nt, p.J - it.j0) : it.valid;   // columns to store
-            const int units = (it.nt / 16 + G - 1 - g) / G;
-            uint64_t acc[NU][8];   // pairs of fp32
+        if constexpr (FP8) {
+            constexpr int NG = (BN / 32 + G - 1) / G;   // groups of 32 columns per warp
+            // the thread's four rows of a quarter: r0, r0 + dr, ...
+            const int r0 = p.quads ? lane & ~3 : lane >> 2, dr = p.quads ? 1 : 8;
+            int x = 0;                                  // slots of scales used so far
+            for (int item = first; item < total && ok; item += step) {
+                const GemmItem it = gemm_item<MODE, CG, BN>(sm, p, item);
+                const int groups = ((it.nt + 31) / 32 + G - 1 - g) / G;
+                float acc[NG][2][16];   // [h]: lanes 16 h + ...
 #pragma unroll
-            for (int i = 0; i < NU; ++i)
+                for (int i = 0; i < NG; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) acc[i][j] = 0;
-            for (int kb = 0; kb < it.kblocks; kb += part, ++u) {
-                const int slot = u % kGemmXsSlots;   // fp8: uses and K blocks are the same
-                uint64_t ws2 = 0;
-                if (FP8) {
-                    if (!gemm_wait(&sm.scfull[slot], (u / kGemmXsSlots) & 1, abort_flag)) { ok = false; break; }
-                    const float w = sm.ws[slot][q * 32 + lane];
-                    ws2 = pack2(w, w);
+                    for (int j = 0; j < 32; ++j) acc[i][j >> 4][j & 15] = 0.0f;
+                for (int kb = 0; kb < it.kblocks; ++kb, ++u) {
+                    const int slot = x % kGemmXsSlots;
+                    if ((kb & 3) == 0 && !gemm_wait_warp(&sm.scfull[slot], (x / kGemmXsSlots) & 1, abort_flag)) { ok = false; break; }
+                    if (!gemm_wait_warp(&sm.accfull[u & 1], (u >> 1) & 1, abort_flag)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (u & 1) * BN + g * 32;
+                    const float *xs = &sm.xs[slot][kb & 3][g * 32], *ws = &sm.ws[slot][kb & 3][q * 32 + r0];
+                    const uint64_t w[2] = {pack2(ws[0], ws[dr]), pack2(ws[2 * dr], ws[3 * dr])};
+                    // all of a warp's groups, or half of them: a condition per group would cost a
+                    // select per sum
+                    if (2 * groups > NG) gemm_add_scaled<NG, NG, G>(acc, t, xs, w);
+                    else if (groups > 0) gemm_add_scaled<NG, (NG + 1) / 2, G>(acc, t, xs, w);
+                    tc_fence_before();
+                    __syncwarp();
+                    const bool sc_done = (kb & 3) == 3 || kb + 1 == it.kblocks;
+                    if (CG == 2) mbar_arrive_remote_lane0(lead_empty0 + 8 * (u & 1));
+                    else if (lane == 0) mbar_arrive(&sm.accempty[u & 1]);
+                    if (sc_done) {
+                        if (lane == 0) mbar_arrive(&sm.scempty[slot]);
+                        ++x;
+                    }
                 }
-                if (!gemm_wait(&sm.accfull[u & 1], (u >> 1) & 1, abort_flag)) { ok = false; break; }
-                tc_fence_after();
-                const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (u & 1) * BN + g * 16;
+                if (!ok) break;
+                const int m = it.m0 + (int)rank * 128 + q * 32 + r0, j = g * 32 + (lane & 3);
+                const int64_t o = (int64_t)(it.j0 + j) * p.ldo + m;
+                auto store = [&](auto f32) {
 #pragma unroll
-                for (int i = 0; i < NU; ++i) {
-                    if (i < units) {
-                        uint32_t c[16];
-                        tmem_ld16(t + i * (16 * G), c);
-                        tmem_wait_ld16(c);
-                        if (FP8) {
-                            const uint32_t xs4 = smem_u32(&sm.xs[slot][(i * G + g) * 16]);
+                    for (int i = 0; i < NG; ++i) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                uint64_t f0, f1;   // volatile: four scales at a time, not all sixteen, in registers
-                                asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(f0), "=l"(f1) : "r"(xs4 + 16 * j));
-                                acc[i][2 * j] = fma2(mul2(pack2u(c[4 * j], c[4 * j + 1]), f0), ws2, acc[i][2 * j]);
-                                acc[i][2 * j + 1] = fma2(mul2(pack2u(c[4 * j + 2], c[4 * j + 3]), f1), ws2, acc[i][2 * j + 1]);
+                        for (int k = 0; k < 8; ++k) {
+                            const int col = i * (32 * G) + 4 * k;   // j columns further for this thread
+                            const int64_t at = o + (int64_t)col * p.ldo;
+                            const float v[4] = {acc[i][0][2 * k], acc[i][0][2 * k + 1], acc[i][1][2 * k], acc[i][1][2 * k + 1]};
+                            if (p.vec) {
+                                gemm_store4<f32.value>(p, at, v, m < p.M && j + col < it.valid);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    gemm_store<f32.value>(p, at + e * dr, v[e], m + e * dr < p.M && j + col < it.valid);
                             }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) acc[i][j] = add2(acc[i][j], pack2u(c[2 * j], c[2 * j + 1]));
                         }
                     }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (CG == 2) mbar_arrive_remote(lead_empty0 + 8 * (u & 1));
-                    else mbar_arrive(&sm.accempty[u & 1]);
-                    if (FP8) mbar_arrive(&sm.scempty[slot]);
-                }
+                };
+                if (p.out_fp32) store(std::true_type{});
+                else store(std::false_type{});
             }
-            if (!ok) break;
-            int64_t o = (int64_t)it.j0 * p.ldo + m;
-            if (MODE == kGemmWgrad) o += (int64_t)it.e * p.out_estride;
-            // stores in program order (volatile), so that the compiler does not hold many of their
-            // addresses and converted values at once and spill
-            const int lim = mok ? jn : 0;
-            if (p.out_fp32) {
-                float *d = reinterpret_cast<float *>(p.out) + o + (int64_t)(g * 16) * p.ldo;
+        } else {
+            constexpr int NU = BN / (16 * G);   // units of 16 columns per warp
+            const int part = p.part;
+            for (int item = first; item < total && ok; item += step) {
+                const GemmItem it = gemm_item<MODE, CG, BN>(sm, p, item);
+                const int m = it.m0 + (int)rank * 128 + q * 32 + lane;
+                const int jn = MODE == kGemmWgrad ? min(it.nt, p.J - it.j0) : it.valid;   // columns to store
+                const int units = (it.nt / 16 + G - 1 - g) / G;
+                float acc[NU][16];
 #pragma unroll
-                for (int i = 0; i < NU; ++i, d += 16 * (G - 1) * p.ldo) {
+                for (int i = 0; i < NU; ++i)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j, d += p.ldo) {
-                        float v = half2of(acc[i][j >> 1], j & 1);
-                        const bool on = (i * G + g) * 16 + j < lim;
-                        if (MODE == kGemmWgrad) {   // read by a later kernel at most: first to leave L2
-                            if (p.accumulate && on) v += *d;
-                            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.global.cs.f32 [%0], %1;\n\t}" ::"l"(d),
-                                         "f"(v), "r"((uint32_t)on)
-                                         : "memory");
-                        } else {
-                            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.global.f32 [%0], %1;\n\t}" ::"l"(d),
-                                         "f"(v), "r"((uint32_t)on)
-                                         : "memory");
+                    for (int j = 0; j < 16; ++j) acc[i][j] = 0.0f;
+                for (int kb = 0; kb < it.kblocks; kb += part, ++u) {
+                    if (!gemm_wait_warp(&sm.accfull[u & 1], (u >> 1) & 1, abort_flag)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (u & 1) * BN + g * 16;
+                    if (2 * units > NU) gemm_add_part<NU, NU, G>(acc, t);
+                    else if (units > 0) gemm_add_part<NU, (NU + 1) / 2, G>(acc, t);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (CG == 2) mbar_arrive_remote(lead_empty0 + 8 * (u & 1));
+                        else mbar_arrive(&sm.accempty[u & 1]);
+                    }
+                }
+                if (!ok) break;
+                int64_t o = (int64_t)(it.j0 + g * 16) * p.ldo + m;
+                if (MODE == kGemmWgrad) o += (int64_t)it.e * p.out_estride;
+                const int lim = m < p.M ? jn : 0;
+                auto store = [&](auto f32) {
+#pragma unroll
+                    for (int i = 0; i < NU; ++i) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j, o += p.ldo) {
+                            const bool on = (i * G + g) * 16 + j < lim;
+                            if (MODE == kGemmWgrad && f32.value && p.accumulate && on)
+                                acc[i][j] += reinterpret_cast<const float *>(p.out)[o];
+                            gemm_store<f32.value, MODE == kGemmWgrad>(p, o, acc[i][j], on);
                         }
+                        o += 16 * (G - 1) * p.ldo;
                     }
-                }
-            } else {
-                __nv_bfloat16 *d = reinterpret_cast<__nv_bfloat16 *>(p.out) + o + (int64_t)(g * 16) * p.ldo;
-#pragma unroll
-                for (int i = 0; i < NU; ++i, d += 16 * (G - 1) * p.ldo) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j, d += p.ldo) {
-                        const bool on = (i * G + g) * 16 + j < lim;
-                        asm volatile(
-                            "{\n\t.reg .pred p;\n\t.reg .b16 h;\n\tsetp.ne.u32 p, %2, 0;\n\tcvt.rn.bf16.f32 h, %1;\n\t"
-                            "@p st.global.b16 [%0], h;\n\t}" ::"l"(d),
-                            "f"(half2of(acc[i][j >> 1], j & 1)), "r"((uint32_t)on)
-                            : "memory");
-                    }
-                }
+                };
+                if (p.out_fp32) store(std::true_type{});
+                else store(std::false_type{});
             }
         }
     }
@@ -693,40 +864,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
 }
 
 // ------------------------------------------------------------------ launch
-
-template <int MODE, int CG, int BN>
-static moe_status gemm_launch(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &b128, GemmParams p, int64_t items, int nsm,
-                              cudaStream_t st) {
-    constexpr int STAGE = kGemmABytes + BN / CG * 128;
-    constexpr int kSmemMax = 227 * 1024;
-    p.stages = std::min<int>(kGemmMaxStages, (kSmemMax - 1024 - (int)sizeof(GemmSmem)) / STAGE);
-    p.m_tiles = (p.M + 128 * CG - 1) / (128 * CG);
-    // The tensor core truncates as it adds, an error that grows with the length of the sum: fp32
-    // results add up parts of 512 in rounded fp32 (K = 4096: 4.4e-6 off in the 2-norm without).
-    p.part = p.out_fp32 ? 8 : 1 << 30;
-    const size_t smem = (size_t)p.stages * STAGE + sizeof(GemmSmem) + 1024;
-    constexpr auto kern = gemm_kernel<MODE, CG, BN>;
-    cudaError_t e = ensure_max_smem<kern>((int)smem);
-    if (e != cudaSuccess) return set_cuda_error(e, "grouped product shared memory");
-    const int64_t groups = std::max<int64_t>(1, std::min<int64_t>(items * p.m_tiles, nsm / CG));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(groups * CG));
-    cfg.blockDim = dim3(gemm_threads(BN));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = CG > 1 ? 2 : 1;
-    count_launch();
-    e = cudaLaunchKernelEx(&cfg, kern, a, b, b128, p);
-    return e == cudaSuccess ? MOE_OK : set_cuda_error(e, "grouped product launch");
-}
 
 // 2D map of a row-major matrix [rows][cols] with `ld` elements per row.
 static moe_status gemm_map2(CUtensorMap *m, int esz, const void *base, int64_t rows, int64_t cols, int64_t ld,
@@ -747,24 +884,23 @@ static moe_status gemm_map3(CUtensorMap *m, int esz, const void *base, int64_t E
                      strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Most row tiles that n_rows rows of E experts can make.
-static int64_t gemm_row_tiles(int n_rows, int E, int BN) {
-    return (int64_t)n_rows / BN + std::min(n_rows, E);
+// One-byte weights [E][rows][cols] for gemm_tma_5d: 128 rows by 128 columns a box.
+static moe_status gemm_map_quads(CUtensorMap *m, const void *base, int64_t E, int64_t rows, int64_t cols, int64_t ld,
+                                 int64_t estride) {
+    const uint64_t dims[5] = {(uint64_t)cols, 8, 4, (uint64_t)(rows / 32), (uint64_t)E};
+    const uint64_t strides[4] = {(uint64_t)(4 * ld), (uint64_t)ld, (uint64_t)(32 * ld), (uint64_t)estride};
+    const uint32_t box[5] = {128, 8, 4, 4, 1};
+    return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int MODE>
-static moe_status gemm_pick(const CUtensorMap &am, const CUtensorMap &bm, const CUtensorMap &bm2, const GemmParams &p, int n, int E, int nsm, cudaStream_t st) {
-    const char *v = getenv("GCFG");
-    const int c = v ? atoi(v) : 2;
-    const bool wg = MODE == kGemmWgrad;
-    if constexpr (MODE != kGemmWgrad) { if (c == 0) return gemm_launch<MODE, 1, 32>(am, bm, bm2, p, gemm_row_tiles(n, E, 32), nsm, st); }
-    const int64_t it = wg ? (int64_t)E * p.j_tiles : gemm_row_tiles(n, E, 256);
-    if (c == 1) return gemm_launch<MODE, 1, 256>(am, bm, bm2, p, it, nsm, st);
-    return gemm_launch<MODE, 2, 256>(am, bm, bm2, p, it, nsm, st);
-}
-
-moe_status launch_grouped_gemm(const GemmArgs &a, int nsm, cudaStream_t st) {
-    CUtensorMap am, bm, bm2;
+// One configuration: CG CTAs per tile (128 m's each), tiles of up to BN j's.
+template <int MODE, int CG, int BN>
+static moe_status gemm_launch(const GemmArgs &a, int nsm, cudaStream_t st) {
+    constexpr bool FP8 = MODE == kGemmFp8;
+    constexpr int STAGE = kGemmABytes + BN / CG * 128, BIG = gemm_big_box(BN / CG);
+    constexpr int kSmemMax = 227 * 1024, esz = FP8 ? 1 : 2, cb = 128 / esz;
+    const int N = a.N, K = a.K;
+    CUtensorMap am, bm, bbig;
     GemmParams p;
     memset(&p, 0, sizeof(p));
     p.offsets = a.offsets;
@@ -774,105 +910,212 @@ moe_status launch_grouped_gemm(const GemmArgs &a, int nsm, cudaStream_t st) {
     p.ldo = a.ldo;
     p.out_fp32 = a.out_fp32;
     moe_status r;
-    const int N = a.N, K = a.K;
-    if (a.op == kGemmOpForward || a.op == kGemmOpFp8) {
-        const int esz = a.op == kGemmOpFp8 ? 1 : 2, cb = 128 / esz;
-        if ((r = gemm_map3(&am, esz, a.w, a.E, N, K, a.ldw, a.w_estride, cb, 128)) != MOE_OK) return r;
-        if ((r = gemm_map2(&bm, esz, a.x, a.n_rows, K, a.ldx, cb, kGemmBoxRows)) != MOE_OK) return r;
-        if ((r = gemm_map2(&bm2, esz, a.x, a.n_rows, K, a.ldx, cb, 128)) != MOE_OK) return r;
-        p.M = N;
-        p.C = K;
+    int64_t tiles = (int64_t)a.n_rows / BN + std::min(a.n_rows, a.E);   // most row tiles that the rows can make
+    if (MODE == kGemmWgrad) {
+        if ((r = gemm_map2(&am, 2, a.w, a.n_rows, K, a.ldw, 64, 64)) != MOE_OK) return r;
+        if ((r = gemm_map2(&bm, 2, a.x, a.n_rows, N, a.ldx, 64, 64)) != MOE_OK) return r;
+        bbig = bm;   // not used
+        p.M = K;
+        p.J = N;
+        p.j_tiles = (N + BN - 1) / BN;
+        p.out_estride = a.out_estride;
+        p.accumulate = a.accumulate;
+        tiles = (int64_t)a.E * p.j_tiles;
+    } else {
+        const bool dgrad = MODE == kGemmDgrad;
+        p.M = dgrad ? K : N;
+        p.C = dgrad ? N : K;
+        // fp8 weights of whole groups of 32 rows arrive in an order that gives each epilogue thread
+        // four neighbouring rows, so that it stores 8 or 16 bytes at a time
+        p.quads = FP8 && N % 32 == 0;
+        const int osz = a.out_fp32 ? 4 : 2;
+        p.vec = p.quads && a.ldo % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % (4 * osz) == 0;
+        r = p.quads ? gemm_map_quads(&am, a.w, a.E, N, K, a.ldw, a.w_estride)
+                    : gemm_map3(&am, esz, a.w, a.E, N, K, a.ldw, a.w_estride, cb, dgrad ? 64 : 128);
+        if (r != MOE_OK) return r;
+        if ((r = gemm_map2(&bm, esz, a.x, a.n_rows, p.C, a.ldx, cb, kGemmBoxRows)) != MOE_OK) return r;
+        if ((r = gemm_map2(&bbig, esz, a.x, a.n_rows, p.C, a.ldx, cb, BIG)) != MOE_OK) return r;
         p.xs = a.xs;
         p.ws = a.ws;
         p.xs_ld = p.ws_ld = (K + 127) / 128;
         p.ws_estride = a.ws_estride;
-        if (a.op == kGemmOpFp8) return gemm_pick<kGemmFp8>(am, bm, bm2, p, a.n_rows, a.E, nsm, st);
-        return gemm_pick<kGemmFwd>(am, bm, bm2, p, a.n_rows, a.E, nsm, st);
     }
-    if (a.op == kGemmOpDgrad) {
-        if ((r = gemm_map3(&am, 2, a.w, a.E, N, K, a.ldw, a.w_estride, 64, 64)) != MOE_OK) return r;
-        if ((r = gemm_map2(&bm, 2, a.x, a.n_rows, N, a.ldx, 64, kGemmBoxRows)) != MOE_OK) return r;
-        if ((r = gemm_map2(&bm2, 2, a.x, a.n_rows, N, a.ldx, 64, 128)) != MOE_OK) return r;
-        p.M = K;
-        p.C = N;
-        return gemm_pick<kGemmDgrad>(am, bm, bm2, p, a.n_rows, a.E, nsm, st);
+    p.stages = std::min<int>(kGemmMaxStages, (kSmemMax - 1024 - (int)sizeof(GemmSmem)) / STAGE);
+    p.m_tiles = (p.M + 128 * CG - 1) / (128 * CG);
+    // The tensor core truncates as it adds, an error that grows with the length of the sum: fp32
+    // results add up parts of 512 in rounded fp32 (K = 4096: 4.4e-6 off in the 2-norm without).
+    p.part = p.out_fp32 ? 8 : 1 << 30;
+    const size_t smem = (size_t)p.stages * STAGE + sizeof(GemmSmem) + 1024;
+    constexpr auto kern = gemm_kernel<MODE, CG, BN>;
+    cudaError_t e = ensure_max_smem<kern>((int)smem);
+    if (e != cudaSuccess) return set_cuda_error(e, "grouped product shared memory");
+    const int64_t groups = std::max<int64_t>(1, std::min<int64_t>(tiles * p.m_tiles, nsm / CG));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(groups * CG));
+    cfg.blockDim = dim3(gemm_threads(FP8, BN));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG > 1 ? 2 : 1;
+    count_launch();
+    e = cudaLaunchKernelEx(&cfg, kern, am, bm, bbig, p);
+    return e == cudaSuccess ? MOE_OK : set_cuda_error(e, "grouped product launch");
+}
+
+// Tiles of up to 64 rows on single CTAs where experts have up to 48 rows on average, else pairs
+// of CTAs (256 m's) with tiles of up to BN rows. The products of few rows are bound by reading
+// the weights, which single CTAs with more stages do a little faster (E = 32, K = 2048, N = 1536,
+// 16 rows each: 40.9 against 42.4 us, fp8 24.7 against 32.2); with more rows the small tile has
+// to read them, and the rows, again and again (64 rows: 45.8 against 46.8 us, fp8 35.9 against
+// 41.0; 128 rows: 76 against 49 us, fp8 59 against 48).
+template <int MODE, int BN>
+static moe_status gemm_pick(const GemmArgs &a, int nsm, cudaStream_t st) {
+    if (a.n_rows <= 48 * (int64_t)a.E) return gemm_launch<MODE, 1, 64>(a, nsm, st);
+    return gemm_launch<MODE, 2, BN>(a, nsm, st);
+}
+
+moe_status launch_grouped_gemm(const GemmArgs &a, int nsm, cudaStream_t st) {
+    switch (a.op) {
+        case kGemmOpForward: return gemm_pick<kGemmFwd, 256>(a, nsm, st);
+        case kGemmOpDgrad: return gemm_pick<kGemmDgrad, 256>(a, nsm, st);
+        case kGemmOpWgrad: return gemm_launch<kGemmWgrad, 2, 256>(a, nsm, st);
+        default: return gemm_pick<kGemmFp8, 192>(a, nsm, st);
     }
-    if ((r = gemm_map2(&am, 2, a.w, a.n_rows, K, a.ldw, 64, 64)) != MOE_OK) return r;
-    if ((r = gemm_map2(&bm, 2, a.x, a.n_rows, N, a.ldx, 64, 64)) != MOE_OK) return r;
-    bm2 = bm;   // not used
-    p.M = K;
-    p.J = N;
-    p.j_tiles = (N + 255) / 256;
-    p.out_estride = a.out_estride;
-    p.accumulate = a.accumulate;
-    return gemm_pick<kGemmWgrad>(am, bm, bm2, p, a.n_rows, a.E, nsm, st);
 }
 
 // ------------------------------------------------------------------ FP8 quantiser
+// Bound by memory (3.03 bytes an element, 5.03 with SwiGLU) once the arithmetic per element is
+// short: 16 elements a lane, so that a block's scale and addresses are worked out by 8 lanes
+// and not by 16, maxima on pairs of bf16 and quotients by a reciprocal. The codes and scales
+// are those of correctly rounded fp32 operations bit for bit.
 
-// One half-warp per block of 128: 8 elements per lane. Each step is one correctly rounded
-// fp32 operation, so the codes and scales are the formula's bit for bit.
+constexpr int kQuantAhead = 2;   // blocks of a lane group whose loads are under way at a time
+
+// RN(v / s) from r = RN(1 / s): Markstein's method (IBM J. Res. Dev. 34, 1990), exact while
+// nothing over- or underflows on the way.
+__device__ __forceinline__ float quotient(float v, float s, float r) {
+    const float q = __fmul_rn(v, r);
+    return __fmaf_rn(__fmaf_rn(-q, s, v), r, q);
+}
+
+__device__ __forceinline__ uint32_t e4m3x4_code(float a, float b, float c, float d) {
+    uint32_t w;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(w)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return w;
+}
+
+// Eight lanes have a block of 128, 16 elements each; the next block of a lane group is drow rows
+// and dkb blocks further.
 template <bool SWIGLU>
-__global__ void __launch_bounds__(256) quantize_fp8_kernel(const __nv_bfloat16 *x, int64_t ldx, int rows, int K,
-                                                           uint8_t *codes, int64_t ldc, float *scale) {
+__global__ void __launch_bounds__(256) quantize_fp8_kernel(const __nv_bfloat16 *x, int64_t ldx, int rows, int K, int KB,
+                                                           int drow, int dkb, uint8_t *codes, int64_t ldc, float *scale) {
     pdl_wait();
     if (threadIdx.x == 0) pdl_release();
-    const int KB = (K + 127) / 128;
-    const int64_t total = (int64_t)rows * KB;
-    const int l16 = threadIdx.x & 15;
-    const int64_t stride = (int64_t)gridDim.x * 16;
-    // whole half-warps leave the loop together with their partner (the shuffles name 32 lanes)
-    const int64_t rounds = (total + stride - 1) / stride;
-    for (int64_t i = 0; i < rounds; ++i) {
-        const int64_t blk = i * stride + (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-        const bool on = blk < total;
-        const int64_t row = on ? blk / KB : 0;
-        const int kb = on ? (int)(blk - row * KB) : 0, c0 = kb * 128 + l16 * 8;
-        float v[8];
+    const int l8 = threadIdx.x & 7;
+    const int64_t first = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
+    int64_t row = first / KB;
+    int kb = (int)(first - row * KB);
+    // a warp's lane groups leave the loop together (the shuffles name 32 lanes)
+    while (__any_sync(0xffffffffu, row < rows)) {
+        uint32_t a[kQuantAhead][8], b[SWIGLU ? kQuantAhead : 1][8];
+        int64_t at[kQuantAhead];
+        int c[kQuantAhead];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-        const bool in = on && c0 < K;   // K is a multiple of 16
-        if (in) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(x + row * ldx + c0);
-            const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
+        for (int u = 0; u < kQuantAhead; ++u) {
+            at[u] = row;
+            c[u] = kb;
+            const bool in = row < rows && kb * 128 + l8 * 16 < K;   // K is a multiple of 16
+            const __nv_bfloat16 *src = x + row * ldx + kb * 128 + l8 * 16;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[2 * j] = __uint_as_float(aw[j] << 16);
-                v[2 * j + 1] = __uint_as_float(aw[j] & 0xFFFF0000u);
-            }
-            if (SWIGLU) {
-                const uint4 b = *reinterpret_cast<const uint4 *>(x + row * ldx + K + c0);
-                const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float u = __uint_as_float(j & 1 ? bw[j >> 1] & 0xFFFF0000u : bw[j >> 1] << 16);
-                    v[j] = v[j] / (1.0f + expf(-v[j])) * u;
+            for (int h = 0; h < 2; ++h) {
+                const uint4 v = in ? __ldcs(reinterpret_cast<const uint4 *>(src) + h) : make_uint4(0u, 0u, 0u, 0u);
+                a[u][4 * h] = v.x;
+                a[u][4 * h + 1] = v.y;
+                a[u][4 * h + 2] = v.z;
+                a[u][4 * h + 3] = v.w;
+                if (SWIGLU) {
+                    const uint4 g = in ? __ldcs(reinterpret_cast<const uint4 *>(src + K) + h) : make_uint4(0u, 0u, 0u, 0u);
+                    b[u][4 * h] = g.x;
+                    b[u][4 * h + 1] = g.y;
+                    b[u][4 * h + 2] = g.z;
+                    b[u][4 * h + 3] = g.w;
                 }
             }
+            row += drow;
+            kb += dkb;
+            if (kb >= KB) {
+                kb -= KB;
+                ++row;
+            }
         }
-        // bit patterns of |v| order like the values, with infinities and NaN on top
-        uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+        for (int u = 0; u < kQuantAhead; ++u) {
+            float v[16];
+            uint32_t top = 0;   // bit patterns of |v| order like the values, infinities and NaN on top
 #pragma unroll
-        for (int d = 8; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float s = top == 0 ? 1.0f : __fdiv_rn(__uint_as_float(top), 448.0f);
-        uint32_t w[2] = {0, 0};
+            for (int j = 0; j < 8; ++j) {
+                v[2 * j] = __uint_as_float(a[u][j] << 16);
+                v[2 * j + 1] = __uint_as_float(a[u][j] & 0xFFFF0000u);
+                if (SWIGLU) {
+                    const float up0 = __uint_as_float(b[u][j] << 16), up1 = __uint_as_float(b[u][j] & 0xFFFF0000u);
+                    v[2 * j] = __fdividef(v[2 * j], 1.0f + expf(-v[2 * j])) * up0;   // 0 where exp(-v) >= 2^126
+                    v[2 * j + 1] = __fdividef(v[2 * j + 1], 1.0f + expf(-v[2 * j + 1])) * up1;
+                    top = max(top, __float_as_uint(v[2 * j]) & 0x7FFFFFFFu);
+                    top = max(top, __float_as_uint(v[2 * j + 1]) & 0x7FFFFFFFu);
+                } else {
+                    top = __vmaxu2(top, a[u][j] & 0x7FFF7FFFu);
+                }
+            }
+            if (!SWIGLU) top = max(top & 0xFFFF0000u, top << 16);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j >> 2] |= e4m3_code(__fdiv_rn(v[j], s)) << (8 * (j & 3));
-        if (in) *reinterpret_cast<uint2 *>(codes + row * ldc + c0) = make_uint2(w[0], w[1]);
-        if (on && l16 == 0) scale[blk] = s;
+            for (int d = 4; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float amax = __uint_as_float(top);
+            float s;
+            // amax between 2^-90 and 2^100: neither a reciprocal nor a remainder leaves fp32's range
+            if (amax > 0x1p-90f && amax < 0x1p100f) {
+                s = quotient(amax, 448.0f, 1.0f / 448.0f);
+                const float r = __frcp_rn(s);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = quotient(v[j], s, r);
+            } else {
+                s = top == 0 ? 1.0f : __fdiv_rn(amax, 448.0f);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = __fdiv_rn(v[j], s);
+            }
+            if (at[u] < rows) {
+                const int c0 = c[u] * 128 + l8 * 16;
+                if (c0 < K)
+                    *reinterpret_cast<uint4 *>(codes + at[u] * ldc + c0) =
+                        make_uint4(e4m3x4_code(v[0], v[1], v[2], v[3]), e4m3x4_code(v[4], v[5], v[6], v[7]),
+                                   e4m3x4_code(v[8], v[9], v[10], v[11]), e4m3x4_code(v[12], v[13], v[14], v[15]));
+                if (l8 == 0) scale[at[u] * KB + c[u]] = s;
+            }
+        }
     }
 }
 
 moe_status launch_quantize_fp8(const void *x, int64_t ldx, int rows, int K, int swiglu, void *codes, int64_t ldc,
                                float *scale, int nsm, cudaStream_t st) {
-    const int64_t blocks = ((int64_t)rows * ((K + 127) / 128) + 15) / 16;
-    const dim3 grid((unsigned)std::min<int64_t>(blocks, (int64_t)nsm * 8));
+    const int KB = (K + 127) / 128;
+    const int64_t blocks = ((int64_t)rows * KB + 31) / 32;
+    const int grid = (int)std::min<int64_t>(blocks, (int64_t)nsm * 4);
+    const int drow = grid * 32 / KB, dkb = grid * 32 % KB;
     const __nv_bfloat16 *xb = reinterpret_cast<const __nv_bfloat16 *>(x);
     uint8_t *cb = reinterpret_cast<uint8_t *>(codes);
-    cudaError_t e = swiglu ? launch_pdl(quantize_fp8_kernel<true>, grid, dim3(256), 0, st, xb, ldx, rows, K, cb, ldc, scale)
-                           : launch_pdl(quantize_fp8_kernel<false>, grid, dim3(256), 0, st, xb, ldx, rows, K, cb, ldc, scale);
+    cudaError_t e = launch_pdl(swiglu ? quantize_fp8_kernel<true> : quantize_fp8_kernel<false>, dim3(grid), dim3(256), 0,
+                               st, xb, ldx, rows, K, KB, drow, dkb, cb, ldc, scale);
     return e == cudaSuccess ? MOE_OK : set_cuda_error(e, "fp8 quantiser launch");
 }
 

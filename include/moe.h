@@ -320,9 +320,9 @@ moe_status moe_grouped_gemm_wgrad(const void *dy, int64_t lddy, const void *x, i
  *   codes: E4M3 bytes [rows][K], ldc bytes a row; scale: fp32 [rows][ceil(K/128)],
  *   dense. moe_dequantize(MOE_FP8_E4M3_K128) reads dense results back (K % 128 == 0,
  *   finite blocks, scales below 128).
- *   Requires K % 16 == 0, ldx % 8 == 0, ldc % 8 == 0 (moe_grouped_gemm_fp8: 16).
+ *   Requires K % 16 == 0, ldx % 8 == 0, ldc % 16 == 0.
  *   rows == 0 is a no-op. Errors: INVALID_ARG for sizes, strides or alignment
- *   outside these (x 16, codes 8, scale 4 bytes) or NULL pointers. */
+ *   outside these (x and codes 16, scale 4 bytes) or NULL pointers. */
 moe_status moe_quantize_fp8(const void *x, int64_t ldx, int rows, int K, int swiglu, void *codes, int64_t ldc,
                             float *scale, moe_stream_t stream);
 

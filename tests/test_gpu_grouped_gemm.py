@@ -264,6 +264,24 @@ def test_strides_padding_and_rows_outside_the_experts(moe, fp32, pad_out):
     assert (big == 7.0).all()
 
 
+@pytest.mark.parametrize("pad_out", [0, 1, 2, 4])
+@pytest.mark.parametrize("rows", [20, 150])
+def test_fp8_results_of_any_alignment(moe, rows, pad_out):
+    """Weight rows in whole groups of 32, whose results are stored four at a time where the result allows."""
+    g = _gen(19)
+    K, N = 256, 160
+    xq, xs, x = _fp8_ints(g, rows, K)
+    wq, ws, w = _fp8_ints(g, N, K)
+    for dt, fp32 in ((BF16, False), (torch.float32, True)):
+        for shift in (0, 1, 4):
+            big = torch.full((rows * (N + pad_out) + 8,), 7.0, dtype=dt, device="cuda")
+            out = big[shift:shift + rows * (N + pad_out)].view(rows, N + pad_out)[:, :N]
+            moe.moe_grouped_gemm_fp8(xq, xs, None, wq, ws, y_fp32=fp32, out=out)
+            _same(out.contiguous(), x.double() @ w.double().T, fp32)
+            out.fill_(7.0)
+            assert (big == 7.0).all()
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_a_row_and_an_expert_keep_their_values_to_themselves(moe, bad):
     """Expert 1's rows and weights are not finite: nothing of them reaches experts 0 and 2, whose rows
