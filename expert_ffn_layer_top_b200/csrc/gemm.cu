@@ -95,8 +95,8 @@ __device__ __forceinline__ void gemm_range(const GemmParams &p, int e, int &beg,
     if (a < 0 || b > p.n_rows || b < a) flag_error(2);
 }
 
-// An expert's n rows are cut into ceil(n / BN) tiles of nearly equal size, a multiple of the
-// MMA's N step, so 260 rows cost two tiles of about 130, not one of 256 and one of 4.
+// An expert's n rows are cut into ceil(n / BN) tiles of equal size, rounded up to the step of
+// the MMA's N, so 260 rows cost two tiles of about 130, not one of 256 and one of 4.
 template <int CG, int BN>
 __device__ __forceinline__ int gemm_tile_rows(int n) {
     const int t = (n + BN - 1) / BN;
@@ -105,15 +105,33 @@ __device__ __forceinline__ int gemm_tile_rows(int n) {
     return (r + G - 1) / G * G;
 }
 
-template <int MODE, int CG, int BN>
+// Tile i of an expert's jt by p.m_tiles: along m first; with STRIPS in strips of kGemmStrip m
+// tiles, so that the tiles at work at a time form a compact block, which reads each operand
+// from HBM a few times only when they do not fit in L2.
+constexpr int kGemmStrip = 16;
+template <bool STRIPS>
+__device__ __forceinline__ void gemm_order(const GemmParams &p, int i, int jt, int &m, int &j) {
+    int width = p.m_tiles, m0 = 0;
+    if (STRIPS) {
+        m0 = i / (kGemmStrip * jt) * kGemmStrip;
+        i -= m0 * jt;
+        width = min(kGemmStrip, p.m_tiles - m0);
+    }
+    j = i / width;
+    m = m0 + i - j * width;
+}
+
+template <int MODE, int CG, int BN, bool STRIPS>
 __device__ __forceinline__ GemmItem gemm_item(const GemmSmem &sm, const GemmParams &p, int item) {
     constexpr int G = 16 * CG;
     GemmItem it;
+    int m, j;
     if (MODE == kGemmWgrad) {
-        const int rt = item / p.m_tiles;
-        it.m0 = (item - rt * p.m_tiles) * (128 * CG);
-        it.e = rt / p.j_tiles;
-        it.j0 = (rt - it.e * p.j_tiles) * BN;
+        const int tiles = p.m_tiles * p.j_tiles;
+        it.e = item / tiles;
+        gemm_order<STRIPS>(p, item - it.e * tiles, p.j_tiles, m, j);
+        it.m0 = m * (128 * CG);
+        it.j0 = j * BN;
         it.row0 = sm.range[it.e].x;
         it.valid = sm.range[it.e].y;
         it.nt = min(BN, (p.J - it.j0 + G - 1) / G * G);
@@ -121,17 +139,23 @@ __device__ __forceinline__ GemmItem gemm_item(const GemmSmem &sm, const GemmPara
         return it;
     }
     const int rt = item / p.m_tiles;
-    it.m0 = (item - rt * p.m_tiles) * (128 * CG);
     int lo = 0, hi = p.E - 1;   // expert with tile_start[e] <= rt < tile_start[e+1]
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (sm.tile_start[mid] <= rt) lo = mid; else hi = mid - 1;
     }
     it.e = lo;
-    const int beg = sm.range[lo].x, n = sm.range[lo].y;
-    const int tr = gemm_tile_rows<CG, BN>(n), t = rt - sm.tile_start[lo];
-    it.row0 = beg + t * tr;
-    it.valid = min(tr, n - t * tr);
+    const int beg = sm.range[lo].x, n = sm.range[lo].y, t0 = sm.tile_start[lo];
+    if (STRIPS) {
+        gemm_order<true>(p, item - t0 * p.m_tiles, sm.tile_start[lo + 1] - t0, m, j);
+    } else {
+        j = rt - t0;
+        m = item - rt * p.m_tiles;
+    }
+    it.m0 = m * (128 * CG);
+    const int tr = gemm_tile_rows<CG, BN>(n);
+    it.row0 = beg + j * tr;
+    it.valid = min(tr, n - j * tr);
     it.j0 = it.row0;
     it.nt = (it.valid + G - 1) / G * G;
     constexpr int CB = MODE == kGemmFp8 ? 128 : 64;
@@ -456,7 +480,7 @@ __device__ __forceinline__ void gemm_add_scaled(float (&acc)[NG][2][16], uint32_
 
 // ------------------------------------------------------------------ kernel
 
-template <int MODE, int CG, int BN>
+template <int MODE, int CG, int BN, bool STRIPS>
 __global__ void __launch_bounds__(gemm_threads(MODE == kGemmFp8, BN), 1)
 gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
             const __grid_constant__ CUtensorMap bbig, GemmParams p) {
@@ -538,13 +562,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
             uint32_t ph = 0;
             bool ok = true;
             for (int item = first; item < total && ok; item += step) {
-                const GemmItem it = gemm_item<MODE, CG, BN>(sm, p, item);
+                const GemmItem it = gemm_item<MODE, CG, BN, STRIPS>(sm, p, item);
                 const int bj0 = it.j0 + (int)rank * (it.nt / CG);          // this CTA's share of B
-                // K-major B in boxes of BIG rows, a smaller rest in boxes of 32: few boxes
-                // when the tile is full (issuing 4 KB boxes only cost a quarter of the rate), no
-                // more than 31 rows too many when it is not
+                // K-major B in boxes of BIG rows, a rest of up to BIG - 64 rows in boxes of 32: each
+                // box takes time to issue (4 KB boxes only: a quarter off the rate; three of them
+                // for 96 rows instead of one of 128: 258 against 242 us for E = 8, 1025 rows each,
+                // K = N = 4096), and a box takes no more than 63 rows too many
                 const int share = it.nt / CG;
-                const int big = BIG > kGemmBoxRows ? (share + 31) / BIG : 0;
+                const int big = BIG > kGemmBoxRows ? (share + 63) / BIG : 0;
                 const int small = big * BIG >= share ? 0 : (share - big * BIG + kGemmBoxRows - 1) / kGemmBoxRows;
                 const int chunks = (share + 63) / 64;
                 const uint32_t bytes = kGemmABytes + (B_MN ? chunks * 8192 : (big * BIG + small * kGemmBoxRows) * 128);
@@ -610,7 +635,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
             uint32_t ph = 0;
             bool ok = true;
             for (int item = first; item < total && ok; item += step) {
-                const GemmItem it = gemm_item<MODE, CG, BN>(sm, p, item);
+                const GemmItem it = gemm_item<MODE, CG, BN, STRIPS>(sm, p, item);
                 const uint32_t idesc = idesc0 | ((uint32_t)(it.nt >> 3) << 17);
                 int left = 0;   // blocks that this accumulator still takes
                 for (int kb = 0; kb < it.kblocks; ++kb) {
@@ -655,7 +680,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
         int x = 0;   // slots filled so far
         bool ok = true;
         for (int item = first; item < total && ok; item += step) {
-            const GemmItem it = gemm_item<MODE, CG, BN>(sm, p, item);
+            const GemmItem it = gemm_item<MODE, CG, BN, STRIPS>(sm, p, item);
             const int r0 = (warp - 2) * 32 + lane, mbase = it.m0 + (int)rank * 128;
             float4 nx[R];
             auto load = [&](int kb) {
@@ -708,7 +733,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
             uint32_t tph = 0;   // bit s: parity of tail[s]
             bool ok = true;
             for (int item = first; item < total && ok; item += step) {
-                const GemmItem it = gemm_item<MODE, CG, BN>(sm, p, item);
+                const GemmItem it = gemm_item<MODE, CG, BN, STRIPS>(sm, p, item);
                 if (!it.kblocks) continue;
                 s = (s + it.kblocks - 1) % ns;   // the stage of the last block
                 if (it.valid & 15) {
@@ -748,7 +773,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
             const int r0 = p.quads ? lane & ~3 : lane >> 2, dr = p.quads ? 1 : 8;
             int x = 0;                                  // slots of scales used so far
             for (int item = first; item < total && ok; item += step) {
-                const GemmItem it = gemm_item<MODE, CG, BN>(sm, p, item);
+                const GemmItem it = gemm_item<MODE, CG, BN, STRIPS>(sm, p, item);
                 const int groups = ((it.nt + 31) / 32 + G - 1 - g) / G;
                 float acc[NG][2][16];   // [h]: lanes 16 h + ...
 #pragma unroll
@@ -805,7 +830,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
             constexpr int NU = BN / (16 * G);   // units of 16 columns per warp
             const int part = p.part;
             for (int item = first; item < total && ok; item += step) {
-                const GemmItem it = gemm_item<MODE, CG, BN>(sm, p, item);
+                const GemmItem it = gemm_item<MODE, CG, BN, STRIPS>(sm, p, item);
                 const int m = it.m0 + (int)rank * 128 + q * 32 + lane;
                 const int jn = MODE == kGemmWgrad ? min(it.nt, p.J - it.j0) : it.valid;   // columns to store
                 const int units = (it.nt / 16 + G - 1 - g) / G;
@@ -894,7 +919,7 @@ static moe_status gemm_map_quads(CUtensorMap *m, const void *base, int64_t E, in
 }
 
 // One configuration: CG CTAs per tile (128 m's each), tiles of up to BN j's.
-template <int MODE, int CG, int BN>
+template <int MODE, int CG, int BN, bool STRIPS = false>
 static moe_status gemm_launch(const GemmArgs &a, int nsm, cudaStream_t st) {
     constexpr bool FP8 = MODE == kGemmFp8;
     constexpr int STAGE = kGemmABytes + BN / CG * 128, BIG = gemm_big_box(BN / CG);
@@ -946,7 +971,7 @@ static moe_status gemm_launch(const GemmArgs &a, int nsm, cudaStream_t st) {
     // results add up parts of 512 in rounded fp32 (K = 4096: 4.4e-6 off in the 2-norm without).
     p.part = p.out_fp32 ? 8 : 1 << 30;
     const size_t smem = (size_t)p.stages * STAGE + sizeof(GemmSmem) + 1024;
-    constexpr auto kern = gemm_kernel<MODE, CG, BN>;
+    constexpr auto kern = gemm_kernel<MODE, CG, BN, STRIPS>;
     cudaError_t e = ensure_max_smem<kern>((int)smem);
     if (e != cudaSuccess) return set_cuda_error(e, "grouped product shared memory");
     const int64_t groups = std::max<int64_t>(1, std::min<int64_t>(tiles * p.m_tiles, nsm / CG));
@@ -975,9 +1000,15 @@ static moe_status gemm_launch(const GemmArgs &a, int nsm, cudaStream_t st) {
 // 16 rows each: 40.9 against 42.4 us, fp8 24.7 against 32.2); with more rows the small tile has
 // to read them, and the rows, again and again (64 rows: 45.8 against 46.8 us, fp8 35.9 against
 // 41.0; 128 rows: 76 against 49 us, fp8 59 against 48).
+// More than kGemmStrip tiles of 256 m's (M > 4096): in strips (8192^3: 715 against 775 us; with
+// fewer, where they would only change the order within an expert, the kernels without the
+// divisions are 1 to 2% faster).
 template <int MODE, int BN>
 static moe_status gemm_pick(const GemmArgs &a, int nsm, cudaStream_t st) {
-    if (a.n_rows <= 48 * (int64_t)a.E) return gemm_launch<MODE, 1, 64>(a, nsm, st);
+    if constexpr (MODE != kGemmWgrad)
+        if (a.n_rows <= 48 * (int64_t)a.E) return gemm_launch<MODE, 1, 64>(a, nsm, st);
+    const int M = MODE == kGemmWgrad || MODE == kGemmDgrad ? a.K : a.N;
+    if (M > kGemmStrip * 256) return gemm_launch<MODE, 2, BN, true>(a, nsm, st);
     return gemm_launch<MODE, 2, BN>(a, nsm, st);
 }
 
@@ -985,7 +1016,7 @@ moe_status launch_grouped_gemm(const GemmArgs &a, int nsm, cudaStream_t st) {
     switch (a.op) {
         case kGemmOpForward: return gemm_pick<kGemmFwd, 256>(a, nsm, st);
         case kGemmOpDgrad: return gemm_pick<kGemmDgrad, 256>(a, nsm, st);
-        case kGemmOpWgrad: return gemm_launch<kGemmWgrad, 2, 256>(a, nsm, st);
+        case kGemmOpWgrad: return gemm_pick<kGemmWgrad, 256>(a, nsm, st);
         default: return gemm_pick<kGemmFp8, 192>(a, nsm, st);
     }
 }

@@ -117,6 +117,24 @@ def test_wgrad_is_exact_on_whole_numbers(moe, counts, K, N, fp32):
         assert torch.equal(out, base + dw)
 
 
+@pytest.mark.parametrize("wide,other", [(4104, 320), (8200, 72)])
+def test_wide_results_in_strips(moe, wide, other):
+    """More than 4096 columns of the result, whose tiles go in strips, several rows of tiles each."""
+    g = _gen(20)
+    counts = [700, 0, 300, 513]
+    R, E, off = sum(counts), len(counts), _offsets(counts)
+    x, w = _ints(g, R, other), _ints(g, E, wide, other)
+    _same(moe.moe_grouped_gemm(x, off, w), _forward64(x, counts, w), False)
+    dy, w = _ints(g, R, other), _ints(g, E, other, wide)
+    _same(moe.moe_grouped_gemm_dgrad(dy, off, w, dx_fp32=True), _dgrad64(dy, counts, w), True)
+    x = _ints(g, R, wide)
+    _same(moe.moe_grouped_gemm_wgrad(dy, x, off), _wgrad64(dy, x, counts), True)
+    K = other // 16 * 16
+    xq, xs, xf = _fp8_ints(g, R, K)
+    wq, ws, wf = _fp8_ints(g, E, wide, K)
+    _same(moe.moe_grouped_gemm_fp8(xq, xs, off, wq, ws), _forward64(xf, counts, wf), False)
+
+
 FP8_SHAPES = [
     ([1], 128, 128), ([1], 16, 8), ([3, 0, 1], 2048, 256), ([0, 0, 5, 0], 144, 520), ([16, 17, 15], 272, 136),
     ([255, 256, 257], 128, 256), ([511, 1, 513, 0, 31], 640, 384), ([1300], 512, 1000), ([64] * 9, 768, 264),
