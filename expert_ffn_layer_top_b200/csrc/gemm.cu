@@ -62,9 +62,9 @@ struct GemmSmem {
     uint64_t empty[kGemmMaxStages];   // the stage's MMAs have read them
     uint64_t tail[kGemmMaxStages];    // wgrad: a stage with rows to clear landed in this CTA
     uint64_t tailpeer[kGemmMaxStages];   // and the pair's other CTA has cleared its own
-    uint64_t accfull[2], accempty[2];
+    uint64_t accfull[4], accempty[4];
     uint64_t scfull[kGemmXsSlots], scempty[kGemmXsSlots];
-    float xs[kGemmXsSlots][4][256];   // fp8: scales of the tile's rows and of this CTA's 128 weight rows
+    float xs[kGemmXsSlots][4][192];   // fp8: scales of the tile's rows and of this CTA's 128 weight rows
     float ws[kGemmXsSlots][4][128];
     uint32_t tmem_base;
     int abort_flag;
@@ -454,22 +454,25 @@ __device__ __forceinline__ void gemm_add_part(float (&acc)[NU][16], uint32_t t) 
 // thread needs a quarter of the columns' scales; with a lane's whole row per thread the copies
 // of them filled the path from shared memory (128 bytes a clock) for longer than the arithmetic
 // takes, two operations an element (384 clocks a block of 192 columns).
-template <int NG, int ACT, int G>
-__device__ __forceinline__ void gemm_add_scaled(float (&acc)[NG][2][16], uint32_t t, const float *xs, const uint64_t (&w)[2]) {
+template <int NG, int ACT, int G, typename F>
+__device__ __forceinline__ void gemm_add_scaled(float (&acc)[NG][2][16], uint32_t t, const float *xs, const uint64_t (&w)[2],
+                                                F &&release) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < ACT; ++i) {
         uint32_t v[16];
         tmem_ld_16x32(t + i * (32 * G), v);
-        float f[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = xs[i * (32 * G) + 4 * k + (lane & 3)];
+        // the scales of a thread's eight columns 4k + T%4 lie next to each other
+        const float4 *xs4 = reinterpret_cast<const float4 *>(xs + i * (32 * G) + 8 * (lane & 3));
+        const float4 fa = xs4[0], fb = xs4[1];
+        const float f[8] = {fa.x, fa.y, fa.z, fa.w, fb.x, fb.y, fb.z, fb.w};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             if (h) tmem_ld_16x32(t + i * (32 * G) + (16u << 16), v);
             tmem_wait_ld16(v);
+            if (i == ACT - 1 && h == 1) release();
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < 8; ++k) {   // (sums kept as pairs made the compiler move and spill them: 15% slower)
                 uint64_t a = pack2(acc[i][h][2 * k], acc[i][h][2 * k + 1]);
                 a = fma2(mul2(pack2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), pack2(f[k], f[k])), w[h], a);
                 unpack2(a, acc[i][h][2 * k], acc[i][h][2 * k + 1]);
@@ -491,7 +494,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
     constexpr int BIG = gemm_big_box(BROWS);
     constexpr int STAGE = kGemmABytes + BROWS * 128;
     constexpr int CB = FP8 ? 128 : 64;                   // c's per stage
-    constexpr uint32_t TMEM_COLS = BN <= 64 ? 128 : 512;   // a power of two with room for two accumulators
+    constexpr int NACC = BN <= 128 ? 4 : 2;              // accumulators
+    constexpr uint32_t TMEM_COLS = BN <= 64 ? 256 : 512;   // a power of two with room for them
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int ns = p.stages;
@@ -509,7 +513,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
             mbar_init(&sm.tail[s], 1);
             mbar_init(&sm.tailpeer[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < NACC; ++b) {
             mbar_init(&sm.accfull[b], 1);
             mbar_init(&sm.accempty[b], CG * EPI);
         }
@@ -642,11 +646,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
                     const bool fresh = left == 0;
                     if (fresh) {
                         left = min(part, it.kblocks - kb);
-                        if (!gemm_wait_warp(&sm.accempty[u & 1], ((u >> 1) & 1) ^ 1, abort_flag)) { ok = false; break; }
+                        if (!gemm_wait_warp(&sm.accempty[u % NACC], ((u / NACC) & 1) ^ 1, abort_flag)) { ok = false; break; }
                     }
                     if (!gemm_wait_warp(&sm.full[s], ph, abort_flag)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t d = tmem + (u & 1) * BN;
+                    const uint32_t d = tmem + (u % NACC) * BN;
                     const uint64_t ad = ad0 + (uint32_t)(s * (STAGE / 16)), bd = bd0 + (uint32_t)(s * (STAGE / 16));
                     const bool last = --left == 0;
                     if (issues) {
@@ -660,7 +664,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
                             gemm_mma<CG, FP8>(d, ad + 3 * AK, bd + 3 * BK, idesc, 1);
                         }
                         gemm_commit<CG>(&sm.empty[s]);
-                        if (last) gemm_commit<CG>(&sm.accfull[u & 1]);
+                        if (last) gemm_commit<CG>(&sm.accfull[u % NACC]);
                     }
                     __syncwarp();
                     if (last) ++u;
@@ -716,7 +720,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
                     for (int i = 0; i < R; ++i) {
                         const int r = r0 + 64 * i, w = r - BN;
                         const float v = b == 0 ? cur[i].x : b == 1 ? cur[i].y : b == 2 ? cur[i].z : cur[i].w;
-                        if (w < 0) sm.xs[slot][b][r] = v;
+                        if (w < 0) sm.xs[slot][b][(r & ~31) | (r & 3) << 3 | (r >> 2 & 7)] = v;   // as gemm_add_scaled reads it
                         else if (w < 128) sm.ws[slot][b][w] = v;
                     }
                 }
@@ -783,20 +787,24 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
                 for (int kb = 0; kb < it.kblocks; ++kb, ++u) {
                     const int slot = x % kGemmXsSlots;
                     if ((kb & 3) == 0 && !gemm_wait_warp(&sm.scfull[slot], (x / kGemmXsSlots) & 1, abort_flag)) { ok = false; break; }
-                    if (!gemm_wait_warp(&sm.accfull[u & 1], (u >> 1) & 1, abort_flag)) { ok = false; break; }
+                    if (!gemm_wait_warp(&sm.accfull[u % NACC], (u / NACC) & 1, abort_flag)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (u & 1) * BN + g * 32;
-                    const float *xs = &sm.xs[slot][kb & 3][g * 32], *ws = &sm.ws[slot][kb & 3][q * 32 + r0];
+                    const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (u % NACC) * BN + g * 32;
+                    const float *xs = &sm.xs[slot][kb & 3][g * 32];
+                    const float *ws = &sm.ws[slot][kb & 3][q * 32 + r0];
                     const uint64_t w[2] = {pack2(ws[0], ws[dr]), pack2(ws[2 * dr], ws[3 * dr])};
                     // all of a warp's groups, or half of them: a condition per group would cost a
                     // select per sum
-                    if (2 * groups > NG) gemm_add_scaled<NG, NG, G>(acc, t, xs, w);
-                    else if (groups > 0) gemm_add_scaled<NG, (NG + 1) / 2, G>(acc, t, xs, w);
-                    tc_fence_before();
-                    __syncwarp();
+                    auto release = [&] {   // the accumulator is read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (CG == 2) mbar_arrive_remote_lane0(lead_empty0 + 8 * (u % NACC));
+                        else if (lane == 0) mbar_arrive(&sm.accempty[u % NACC]);
+                    };
+                    if (2 * groups > NG) gemm_add_scaled<NG, NG, G>(acc, t, xs, w, release);
+                    else if (groups > 0) gemm_add_scaled<NG, (NG + 1) / 2, G>(acc, t, xs, w, release);
+                    else release();
                     const bool sc_done = (kb & 3) == 3 || kb + 1 == it.kblocks;
-                    if (CG == 2) mbar_arrive_remote_lane0(lead_empty0 + 8 * (u & 1));
-                    else if (lane == 0) mbar_arrive(&sm.accempty[u & 1]);
                     if (sc_done) {
                         if (lane == 0) mbar_arrive(&sm.scempty[slot]);
                         ++x;
@@ -840,16 +848,16 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
 #pragma unroll
                     for (int j = 0; j < 16; ++j) acc[i][j] = 0.0f;
                 for (int kb = 0; kb < it.kblocks; kb += part, ++u) {
-                    if (!gemm_wait_warp(&sm.accfull[u & 1], (u >> 1) & 1, abort_flag)) { ok = false; break; }
+                    if (!gemm_wait_warp(&sm.accfull[u % NACC], (u / NACC) & 1, abort_flag)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (u & 1) * BN + g * 16;
+                    const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (u % NACC) * BN + g * 16;
                     if (2 * units > NU) gemm_add_part<NU, NU, G>(acc, t);
                     else if (units > 0) gemm_add_part<NU, (NU + 1) / 2, G>(acc, t);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        if (CG == 2) mbar_arrive_remote(lead_empty0 + 8 * (u & 1));
-                        else mbar_arrive(&sm.accempty[u & 1]);
+                        if (CG == 2) mbar_arrive_remote(lead_empty0 + 8 * (u % NACC));
+                        else mbar_arrive(&sm.accempty[u % NACC]);
                     }
                 }
                 if (!ok) break;
