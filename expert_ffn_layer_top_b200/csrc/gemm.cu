@@ -32,6 +32,9 @@ constexpr int kGemmFwd = 0, kGemmDgrad = 1, kGemmWgrad = 2, kGemmFp8 = 3;
 // (their sums stay in registers from K block to K block; 8 or 16 warps took 6% and 50% longer),
 // 8 for small tiles.
 __host__ __device__ constexpr int gemm_epi_warps(bool fp8, int BN) { return BN <= 64 ? 8 : fp8 ? 12 : 16; }
+// CTAs per SM: two for the smallest tiles, so that one of them, or the next kernel's, sets up and
+// loads while the other computes or stores.
+__host__ __device__ constexpr int gemm_ctas(int BN) { return BN <= 32 ? 2 : 1; }
 __host__ __device__ constexpr int gemm_threads(bool fp8, int BN) { return 128 + 32 * gemm_epi_warps(fp8, BN); }
 constexpr int kGemmABytes = 128 * 128;     // one CTA's A tile of a stage: 128 m x 128 bytes
 constexpr int kGemmBoxRows = 32;           // rows of B in a small TMA box (K-major B)
@@ -57,21 +60,35 @@ struct GemmParams {
     int64_t xs_ld, ws_ld, ws_estride;
 };
 
-struct GemmSmem {
+struct alignas(16) GemmSmem {
     uint64_t full[kGemmMaxStages];    // operands of a stage landed (and tail rows cleared)
     uint64_t empty[kGemmMaxStages];   // the stage's MMAs have read them
     uint64_t tail[kGemmMaxStages];    // wgrad: a stage with rows to clear landed in this CTA
     uint64_t tailpeer[kGemmMaxStages];   // and the pair's other CTA has cleared its own
     uint64_t accfull[4], accempty[4];
     uint64_t scfull[kGemmXsSlots], scempty[kGemmXsSlots];
-    float xs[kGemmXsSlots][4][192];   // fp8: scales of the tile's rows and of this CTA's 128 weight rows
-    float ws[kGemmXsSlots][4][128];
     uint32_t tmem_base;
     int abort_flag;
     int total_items;
-    int tile_start[kMaxExperts + 1];
-    int2 range[kMaxExperts];          // first row and rows of each expert
 };
+
+// Behind it: each expert's first row and rows (int2) and its first row tile (int, one more), for
+// E experts where shared memory is short, else for kMaxExperts (a fixed place, which saves the
+// epilogue registers); and, for fp8, kGemmXsSlots times four K blocks' scales of the tile's rows
+// ([BN]) and of the CTA's weight rows ([128]).
+template <int BN>
+__host__ __device__ constexpr int gemm_table(int E) { return BN <= 32 ? E : kMaxExperts; }
+template <int BN>
+__host__ __device__ constexpr int gemm_tables_bytes(int E) { return ((gemm_table<BN>(E) + 1) * 12 + 15) & ~15; }
+template <bool FP8, int BN>
+__host__ __device__ constexpr int gemm_smem_bytes(int E) {
+    return (int)sizeof(GemmSmem) + gemm_tables_bytes<BN>(E) + (FP8 ? kGemmXsSlots * 4 * (BN + 128) * 4 : 0);
+}
+__device__ __forceinline__ const int2 *gemm_ranges(const GemmSmem &sm) { return reinterpret_cast<const int2 *>(&sm + 1); }
+template <int BN>
+__device__ __forceinline__ const int *gemm_tile_starts(const GemmSmem &sm, const GemmParams &p) {
+    return reinterpret_cast<const int *>(gemm_ranges(sm) + gemm_table<BN>(p.E));
+}
 
 struct GemmItem {
     int e, m0;      // expert, first m of the CTA group's tile
@@ -123,6 +140,8 @@ __device__ __forceinline__ void gemm_order(const GemmParams &p, int i, int jt, i
 
 template <int MODE, int CG, int BN, bool STRIPS>
 __device__ __forceinline__ GemmItem gemm_item(const GemmSmem &sm, const GemmParams &p, int item) {
+    const int2 *range = gemm_ranges(sm);
+    const int *tile_start = gemm_tile_starts<BN>(sm, p);
     constexpr int G = 16 * CG;
     GemmItem it;
     int m, j;
@@ -132,8 +151,8 @@ __device__ __forceinline__ GemmItem gemm_item(const GemmSmem &sm, const GemmPara
         gemm_order<STRIPS>(p, item - it.e * tiles, p.j_tiles, m, j);
         it.m0 = m * (128 * CG);
         it.j0 = j * BN;
-        it.row0 = sm.range[it.e].x;
-        it.valid = sm.range[it.e].y;
+        it.row0 = range[it.e].x;
+        it.valid = range[it.e].y;
         it.nt = min(BN, (p.J - it.j0 + G - 1) / G * G);
         it.kblocks = (it.valid + 63) / 64;
         return it;
@@ -142,12 +161,12 @@ __device__ __forceinline__ GemmItem gemm_item(const GemmSmem &sm, const GemmPara
     int lo = 0, hi = p.E - 1;   // expert with tile_start[e] <= rt < tile_start[e+1]
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (sm.tile_start[mid] <= rt) lo = mid; else hi = mid - 1;
+        if (tile_start[mid] <= rt) lo = mid; else hi = mid - 1;
     }
     it.e = lo;
-    const int beg = sm.range[lo].x, n = sm.range[lo].y, t0 = sm.tile_start[lo];
+    const int beg = range[lo].x, n = range[lo].y, t0 = tile_start[lo];
     if (STRIPS) {
-        gemm_order<true>(p, item - t0 * p.m_tiles, sm.tile_start[lo + 1] - t0, m, j);
+        gemm_order<true>(p, item - t0 * p.m_tiles, tile_start[lo + 1] - t0, m, j);
     } else {
         j = rt - t0;
         m = item - rt * p.m_tiles;
@@ -484,7 +503,7 @@ __device__ __forceinline__ void gemm_add_scaled(float (&acc)[NG][2][16], uint32_
 // ------------------------------------------------------------------ kernel
 
 template <int MODE, int CG, int BN, bool STRIPS>
-__global__ void __launch_bounds__(gemm_threads(MODE == kGemmFp8, BN), 1)
+__global__ void __launch_bounds__(gemm_threads(MODE == kGemmFp8, BN), gemm_ctas(BN))
 gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
             const __grid_constant__ CUtensorMap bbig, GemmParams p) {
     constexpr bool FP8 = MODE == kGemmFp8;
@@ -495,11 +514,13 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
     constexpr int STAGE = kGemmABytes + BROWS * 128;
     constexpr int CB = FP8 ? 128 : 64;                   // c's per stage
     constexpr int NACC = BN <= 128 ? 4 : 2;              // accumulators
-    constexpr uint32_t TMEM_COLS = BN <= 64 ? 256 : 512;   // a power of two with room for them
+    constexpr uint32_t TMEM_COLS = BN <= 32 ? 128 : BN <= 64 ? 256 : 512;   // a power of two with room for them
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int ns = p.stages;
     GemmSmem &sm = *reinterpret_cast<GemmSmem *>(ring + ns * STAGE);
+    float *xs_s = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(&sm + 1) + gemm_tables_bytes<BN>(p.E));
+    float *ws_s = xs_s + kGemmXsSlots * 4 * BN;
     volatile int *abort_flag = &sm.abort_flag;
     const int warp = warp_id(), lane = lane_id();
     const uint32_t rank = CG == 2 ? cluster_rank() : 0;
@@ -527,27 +548,31 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
         tma_prefetch_desc(&bmap);
         if (MODE != kGemmWgrad && BIG > kGemmBoxRows) tma_prefetch_desc(&bbig);
     }
-    if (warp == 2) gemm_tmem_alloc<CG>(&sm.tmem_base, TMEM_COLS);
     pdl_wait();
     if (threadIdx.x == 0) pdl_release();
+    int2 *range = const_cast<int2 *>(gemm_ranges(sm));
+    int *tile_start = const_cast<int *>(gemm_tile_starts<BN>(sm, p));
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
         int beg, n;
         gemm_range(p, e, beg, n);
-        sm.range[e] = make_int2(beg, n);
+        range[e] = make_int2(beg, n);
     }
     __syncthreads();
+    // (after the wait: a kernel that held TMEM while it waits for one that still has to allocate
+    // its own on the same SM would never end)
+    if (warp == 2) gemm_tmem_alloc<CG>(&sm.tmem_base, TMEM_COLS);
     if (warp == 3) {   // first row tile of each expert
         int run = 0;
-        if (lane == 0) sm.tile_start[0] = 0;
+        if (lane == 0) tile_start[0] = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
             const int e = e0 + lane;
-            int incl = e < p.E ? (sm.range[e].y + BN - 1) / BN : 0;
+            int incl = e < p.E ? (range[e].y + BN - 1) / BN : 0;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int v = __shfl_up_sync(0xffffffffu, incl, d);
                 if (lane >= d) incl += v;
             }
-            if (e < p.E) sm.tile_start[e + 1] = run + incl;
+            if (e < p.E) tile_start[e + 1] = run + incl;
             run += __shfl_sync(0xffffffffu, incl, 31);
         }
         if (lane == 0) sm.total_items = MODE == kGemmWgrad ? p.E * p.j_tiles * p.m_tiles : run * p.m_tiles;
@@ -720,8 +745,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
                     for (int i = 0; i < R; ++i) {
                         const int r = r0 + 64 * i, w = r - BN;
                         const float v = b == 0 ? cur[i].x : b == 1 ? cur[i].y : b == 2 ? cur[i].z : cur[i].w;
-                        if (w < 0) sm.xs[slot][b][(r & ~31) | (r & 3) << 3 | (r >> 2 & 7)] = v;   // as gemm_add_scaled reads it
-                        else if (w < 128) sm.ws[slot][b][w] = v;
+                        if (w < 0) xs_s[(slot * 4 + b) * BN + ((r & ~31) | (r & 3) << 3 | (r >> 2 & 7))] = v;   // as gemm_add_scaled reads it
+                        else if (w < 128) ws_s[(slot * 4 + b) * 128 + w] = v;
                     }
                 }
                 __syncwarp();
@@ -790,8 +815,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
                     if (!gemm_wait_warp(&sm.accfull[u % NACC], (u / NACC) & 1, abort_flag)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (u % NACC) * BN + g * 32;
-                    const float *xs = &sm.xs[slot][kb & 3][g * 32];
-                    const float *ws = &sm.ws[slot][kb & 3][q * 32 + r0];
+                    const float *xs = xs_s + (slot * 4 + (kb & 3)) * BN + g * 32;
+                    const float *ws = ws_s + (slot * 4 + (kb & 3)) * 128 + q * 32 + r0;
                     const uint64_t w[2] = {pack2(ws[0], ws[dr]), pack2(ws[2 * dr], ws[3 * dr])};
                     // all of a warp's groups, or half of them: a condition per group would cost a
                     // select per sum
@@ -931,7 +956,7 @@ template <int MODE, int CG, int BN, bool STRIPS = false>
 static moe_status gemm_launch(const GemmArgs &a, int nsm, cudaStream_t st) {
     constexpr bool FP8 = MODE == kGemmFp8;
     constexpr int STAGE = kGemmABytes + BN / CG * 128, BIG = gemm_big_box(BN / CG);
-    constexpr int kSmemMax = 227 * 1024, esz = FP8 ? 1 : 2, cb = 128 / esz;
+    constexpr int kSmemMax = gemm_ctas(BN) == 2 ? 113 * 1024 : 227 * 1024, esz = FP8 ? 1 : 2, cb = 128 / esz;
     const int N = a.N, K = a.K;
     CUtensorMap am, bm, bbig;
     GemmParams p;
@@ -973,16 +998,16 @@ static moe_status gemm_launch(const GemmArgs &a, int nsm, cudaStream_t st) {
         p.xs_ld = p.ws_ld = (K + 127) / 128;
         p.ws_estride = a.ws_estride;
     }
-    p.stages = std::min<int>(kGemmMaxStages, (kSmemMax - 1024 - (int)sizeof(GemmSmem)) / STAGE);
+    p.stages = std::min<int>(kGemmMaxStages, (kSmemMax - 1024 - gemm_smem_bytes<FP8, BN>(a.E)) / STAGE);
     p.m_tiles = (p.M + 128 * CG - 1) / (128 * CG);
     // The tensor core truncates as it adds, an error that grows with the length of the sum: fp32
     // results add up parts of 512 in rounded fp32 (K = 4096: 4.4e-6 off in the 2-norm without).
     p.part = p.out_fp32 ? 8 : 1 << 30;
-    const size_t smem = (size_t)p.stages * STAGE + sizeof(GemmSmem) + 1024;
+    const size_t smem = (size_t)p.stages * STAGE + gemm_smem_bytes<FP8, BN>(a.E) + 1024;
     constexpr auto kern = gemm_kernel<MODE, CG, BN, STRIPS>;
     cudaError_t e = ensure_max_smem<kern>((int)smem);
     if (e != cudaSuccess) return set_cuda_error(e, "grouped product shared memory");
-    const int64_t groups = std::max<int64_t>(1, std::min<int64_t>(tiles * p.m_tiles, nsm / CG));
+    const int64_t groups = std::max<int64_t>(1, std::min<int64_t>(tiles * p.m_tiles, gemm_ctas(BN) * nsm / CG));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(groups * CG));
     cfg.blockDim = dim3(gemm_threads(FP8, BN));
@@ -1013,6 +1038,8 @@ static moe_status gemm_launch(const GemmArgs &a, int nsm, cudaStream_t st) {
 // divisions are 1 to 2% faster).
 template <int MODE, int BN>
 static moe_status gemm_pick(const GemmArgs &a, int nsm, cudaStream_t st) {
+    if constexpr (MODE != kGemmWgrad)
+        if (a.n_rows <= 24 * (int64_t)a.E) return gemm_launch<MODE, 1, 32>(a, nsm, st);
     if constexpr (MODE != kGemmWgrad)
         if (a.n_rows <= 48 * (int64_t)a.E) return gemm_launch<MODE, 1, 64>(a, nsm, st);
     const int M = MODE == kGemmWgrad || MODE == kGemmDgrad ? a.K : a.N;
@@ -1053,6 +1080,12 @@ __device__ __forceinline__ uint32_t e4m3x4_code(float a, float b, float c, float
         : "=r"(w)
         : "f"(a), "f"(b), "f"(c), "f"(d));
     return w;
+}
+
+// v / (1 + exp(-v)), with exp(-|v|) <= 1 so that nothing overflows and the divisor is in [1, 2].
+__device__ __forceinline__ float silu(float v) {
+    const float e = expf(-fabsf(v));
+    return __fdividef(v >= 0.0f ? v : v * e, 1.0f + e);
 }
 
 // Eight lanes have a block of 128, 16 elements each; the next block of a lane group is drow rows
@@ -1109,8 +1142,8 @@ __global__ void __launch_bounds__(256) quantize_fp8_kernel(const __nv_bfloat16 *
                 v[2 * j + 1] = __uint_as_float(a[u][j] & 0xFFFF0000u);
                 if (SWIGLU) {
                     const float up0 = __uint_as_float(b[u][j] << 16), up1 = __uint_as_float(b[u][j] & 0xFFFF0000u);
-                    v[2 * j] = __fdividef(v[2 * j], 1.0f + expf(-v[2 * j])) * up0;   // 0 where exp(-v) >= 2^126
-                    v[2 * j + 1] = __fdividef(v[2 * j + 1], 1.0f + expf(-v[2 * j + 1])) * up1;
+                    v[2 * j] = silu(v[2 * j]) * up0;
+                    v[2 * j + 1] = silu(v[2 * j + 1]) * up1;
                     top = max(top, __float_as_uint(v[2 * j]) & 0x7FFFFFFFu);
                     top = max(top, __float_as_uint(v[2 * j + 1]) & 0x7FFFFFFFu);
                 } else {

@@ -81,7 +81,8 @@ def _same(got, want64, fp32):
 SHAPES = [
     ([1], 64, 128), ([1], 8, 8), ([3, 0, 1], 2048, 256), ([0, 0, 5, 0], 128, 520), ([16, 17, 15], 264, 136),
     ([255, 256, 257], 128, 256), ([511, 1, 513, 0, 31], 192, 384), ([1300], 512, 1000), ([64] * 9, 768, 264),
-    ([2, 1] * 40, 256, 512), ([33, 700, 129, 5], 1000, 1160), ([8] * 200, 72, 40),
+    ([2, 1] * 40, 256, 512), ([33, 700, 129, 5], 1000, 1160), ([8] * 200, 72, 40), ([30] * 6, 200, 264),
+    ([1, 0, 2] * 300, 64, 72),
 ]
 
 
@@ -138,7 +139,7 @@ def test_wide_results_in_strips(moe, wide, other):
 FP8_SHAPES = [
     ([1], 128, 128), ([1], 16, 8), ([3, 0, 1], 2048, 256), ([0, 0, 5, 0], 144, 520), ([16, 17, 15], 272, 136),
     ([255, 256, 257], 128, 256), ([511, 1, 513, 0, 31], 640, 384), ([1300], 512, 1000), ([64] * 9, 768, 264),
-    ([2, 1] * 40, 256, 512), ([33, 700, 129, 5], 1008, 1160),
+    ([2, 1] * 40, 256, 512), ([33, 700, 129, 5], 1008, 1160), ([30] * 6, 208, 264), ([1, 0, 2] * 300, 64, 96),
 ]
 
 
@@ -223,6 +224,18 @@ def test_fp8_random_values_stay_within_the_bound(moe, fp32, K):
 
 
 # ---------------------------------------------------------------------------- layouts and neighbours
+
+
+@pytest.mark.parametrize("N", [1, 3, 130])
+@pytest.mark.parametrize("rows", [5, 200])
+def test_results_of_few_or_odd_columns(moe, rows, N):
+    g = _gen(21)
+    x, w = _ints(g, rows, 200), _ints(g, N, 200)
+    for fp32 in (False, True):
+        _same(moe.moe_grouped_gemm(x, None, w, y_fp32=fp32), x.double() @ w.double().T, fp32)
+    xq, xs, xf = _fp8_ints(g, rows, 208)
+    wq, ws, wf = _fp8_ints(g, N, 208)
+    _same(moe.moe_grouped_gemm_fp8(xq, xs, None, wq, ws, y_fp32=True), xf.double() @ wf.double().T, True)
 
 
 def _strided(t, pad, fill):
@@ -470,6 +483,8 @@ def test_swiglu_quantise(moe, rows, K):
     x = (torch.randn(rows, 2 * K, generator=g) * 3).to(BF16)
     x[0, 0], x[0, K] = -90.0, 1.0
     x[0, 1], x[0, K + 1] = 60.0, 0.5
+    if rows > 1:
+        x[1, :K], x[1, K:] = -87.5, 3.0     # exp(87.5) is beyond 2^126: the block's values are tiny, not 0
     codes, scale = moe.moe_quantize_fp8(x.cuda(), swiglu=True)
     gate, up = x[:, :K].double(), x[:, K:].double()
     h = gate / (1 + torch.exp(-gate)) * up
