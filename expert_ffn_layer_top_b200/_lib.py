@@ -319,13 +319,20 @@ def moe_dequantize(fmt: str, w: torch.Tensor, scale: Optional[torch.Tensor], tsc
 _FP8 = (torch.uint8, torch.float8_e4m3fn)
 
 
-def _device(*ts: Optional[torch.Tensor]) -> int:
+_BF16 = (torch.bfloat16,)
+
+
+# The wrappers below are called for every projection of a decode step, where their own time is
+# most of a small product's: each tensor's shape and strides are asked for once.
+
+
+def _device(t: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
     """Index of the one CUDA device that the tensors are on."""
-    d = ts[0].get_device()
+    d = t.get_device()
     if d < 0:
         raise ValueError("device tensors expected")
-    for t in ts:
-        if t is not None and t.get_device() != d:
+    for o in others:
+        if o is not None and o.get_device() != d:
             raise ValueError("tensors on one device expected")
     return d
 
@@ -334,30 +341,44 @@ def _run(d: int, fn, *args):
     """Call fn(*args, stream) on device d and its current stream."""
     if d != torch._C._cuda_getDevice():
         with torch.cuda.device(d):
-            return _check(fn(*args, torch._C._cuda_getCurrentRawStream(d)))
-    status = fn(*args, torch._C._cuda_getCurrentRawStream(d))
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(d))
+    else:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(d))
     if status:
         _check(status)
 
 
-def _matrix(name: str, t: torch.Tensor, dtypes, ndim: int = 2):
-    if t.dtype not in dtypes or t.dim() != ndim:
-        raise ValueError(f"{name}: expected {ndim}-D {' or '.join(str(d) for d in dtypes)}, got {t.dim()}-D {t.dtype}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
+def _refuse(name: str, t: torch.Tensor, dtypes, ndim: int):
+    raise ValueError(f"{name}: expected {ndim}-D {' or '.join(str(d) for d in dtypes)} with a contiguous last dimension, "
+                     f"got {t.dtype} of shape {tuple(t.shape)} and strides {t.stride()}")
 
 
-def _ld(t: torch.Tensor) -> int:
-    """Elements from row to row of a matrix (of each of a batch); a lone row's stride says nothing."""
-    return t.stride(-2) if t.shape[-2] > 1 else -(-t.shape[-1] // 16) * 16
+def _matrix(name: str, t: torch.Tensor, dtypes):
+    """(rows, columns, elements from row to row) of a matrix; a lone row's stride says nothing."""
+    if t.dtype not in dtypes or t.dim() != 2:
+        _refuse(name, t, dtypes, 2)
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        _refuse(name, t, dtypes, 2)
+    return rows, cols, ld if rows > 1 else -(-cols // 16) * 16
 
 
-def _estride(t: torch.Tensor) -> int:
-    if t.shape[0] <= 1:
-        return 0
-    if t.stride(0) == 0:   # 0 means dense in the C ABI
-        raise ValueError("experts expanded from one: pass a copy per expert")
-    return t.stride(0)
+def _batch(name: str, t: torch.Tensor, dtypes):
+    """(E, rows, columns, elements from row to row, from expert to expert) of E matrices, or of one."""
+    if t.dim() == 2:
+        return (1, *_matrix(name, t, dtypes), 0)
+    if t.dtype not in dtypes or t.dim() != 3:
+        _refuse(name, t, dtypes, 3)
+    E, rows, cols = t.shape
+    es, ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        _refuse(name, t, dtypes, 3)
+    if E <= 1:
+        es = 0
+    elif es == 0:   # 0 means dense in the C ABI
+        raise ValueError(f"{name}: experts expanded from one: pass a copy per expert")
+    return E, rows, cols, ld if rows > 1 else -(-cols // 16) * 16, es
 
 
 def _offsets(offsets: Optional[torch.Tensor], E: int):
@@ -366,61 +387,47 @@ def _offsets(offsets: Optional[torch.Tensor], E: int):
         if E != 1:
             raise ValueError("offsets: needed with more than one expert")
         return None
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] != E + 1 or not offsets.is_contiguous():
+    if offsets.dtype != torch.int32 or offsets.shape != (E + 1,) or not offsets.is_contiguous():
         raise ValueError(f"offsets: expected contiguous int32 [{E + 1}]")
     return offsets.data_ptr()
 
 
-def _result(out: Optional[torch.Tensor], shape, fp32: bool, device) -> torch.Tensor:
+def _result(out: Optional[torch.Tensor], rows: int, cols: int, fp32: bool, device):
+    """A [rows, cols] result, `out` if given, and its elements from row to row."""
     dtype = torch.float32 if fp32 else torch.bfloat16
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != shape:
-        raise ValueError(f"out: expected shape {shape}, got {tuple(out.shape)}")
-    _matrix("out", out, (dtype,), len(shape))
-    return out
-
-
-def _experts_of(w: torch.Tensor) -> torch.Tensor:
-    return w.unsqueeze(0) if w.dim() == 2 else w
-
-
-_BF16 = (torch.bfloat16,)
+        return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device), cols
+    if out.shape != (rows, cols):
+        raise ValueError(f"out: expected shape {(rows, cols)}, got {tuple(out.shape)}")
+    return out, _matrix("out", out, (dtype,))[2]
 
 
 def moe_grouped_gemm(x: torch.Tensor, offsets: Optional[torch.Tensor], w: torch.Tensor, y_fp32: bool = False,
                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y[r] = w[e] x[r] for the rows r of expert e; w bf16 [E, N, K] (or [N, K] with offsets None)."""
-    w = _experts_of(w)
-    _matrix("x", x, _BF16)
-    _matrix("w", w, _BF16, 3)
-    E, N, K = w.shape
-    rows = x.shape[0]
-    if x.shape[1] != K:
-        raise ValueError(f"x has {x.shape[1]} columns, w {K}")
+    rows, cols, ldx = _matrix("x", x, _BF16)
+    E, N, K, ldw, es = _batch("w", w, _BF16)
+    if cols != K:
+        raise ValueError(f"x has {cols} columns, w {K}")
     off = _offsets(offsets, E)
     d = _device(x, offsets, w, out)
-    y = _result(out, (rows, N), y_fp32, x.device)
-    _run(d, lib().moe_grouped_gemm, x.data_ptr(), _ld(x), rows, off, w.data_ptr(), _ld(w), _estride(w), E, N, K,
-         y.data_ptr(), _ld(y), int(y_fp32))
+    y, ldy = _result(out, rows, N, y_fp32, x.device)
+    _run(d, lib().moe_grouped_gemm, x.data_ptr(), ldx, rows, off, w.data_ptr(), ldw, es, E, N, K, y.data_ptr(), ldy, y_fp32)
     return y
 
 
 def moe_grouped_gemm_dgrad(dy: torch.Tensor, offsets: Optional[torch.Tensor], w: torch.Tensor, dx_fp32: bool = False,
                            out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dx[r] = w[e]^T dy[r]: the gradient of moe_grouped_gemm for x."""
-    w = _experts_of(w)
-    _matrix("dy", dy, _BF16)
-    _matrix("w", w, _BF16, 3)
-    E, N, K = w.shape
-    rows = dy.shape[0]
-    if dy.shape[1] != N:
-        raise ValueError(f"dy has {dy.shape[1]} columns, w {N} rows")
+    rows, cols, lddy = _matrix("dy", dy, _BF16)
+    E, N, K, ldw, es = _batch("w", w, _BF16)
+    if cols != N:
+        raise ValueError(f"dy has {cols} columns, w {N} rows")
     off = _offsets(offsets, E)
     d = _device(dy, offsets, w, out)
-    dx = _result(out, (rows, K), dx_fp32, dy.device)
-    _run(d, lib().moe_grouped_gemm_dgrad, dy.data_ptr(), _ld(dy), rows, off, w.data_ptr(), _ld(w), _estride(w), E, N, K,
-         dx.data_ptr(), _ld(dx), int(dx_fp32))
+    dx, lddx = _result(out, rows, K, dx_fp32, dy.device)
+    _run(d, lib().moe_grouped_gemm_dgrad, dy.data_ptr(), lddy, rows, off, w.data_ptr(), ldw, es, E, N, K, dx.data_ptr(), lddx,
+         dx_fp32)
     return dx
 
 
@@ -428,37 +435,40 @@ def moe_grouped_gemm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: Optional[
                            out: Optional[torch.Tensor] = None, accumulate: bool = False) -> torch.Tensor:
     """dw[e] = sum of dy[r] x[r]^T over the rows of expert e: the gradient of moe_grouped_gemm for w
     ([E, N, K]; E = 1 with offsets None). accumulate adds to `out`."""
-    _matrix("dy", dy, _BF16)
-    _matrix("x", x, _BF16)
-    rows = x.shape[0]
-    if rows != dy.shape[0]:
-        raise ValueError(f"dy has {dy.shape[0]} rows, x {rows}")
+    rows, N, lddy = _matrix("dy", dy, _BF16)
+    xrows, K, ldx = _matrix("x", x, _BF16)
+    if xrows != rows:
+        raise ValueError(f"dy has {rows} rows, x {xrows}")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     E = 1 if offsets is None else max(offsets.numel() - 1, 0)
-    N, K = dy.shape[1], x.shape[1]
     off = _offsets(offsets, E)
     d = _device(dy, x, offsets, out)
-    dw = _result(out, (E, N, K), dw_fp32, x.device)
-    _run(d, lib().moe_grouped_gemm_wgrad, dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), rows, off, E, N, K,
-         dw.data_ptr(), _ld(dw), _estride(dw), int(dw_fp32), int(accumulate))
-    return dw
+    dtype = torch.float32 if dw_fp32 else torch.bfloat16
+    if out is None:
+        out = torch.empty((E, N, K), dtype=dtype, device=x.device)
+    elif out.shape != (E, N, K):
+        raise ValueError(f"out: expected shape {(E, N, K)}, got {tuple(out.shape)}")
+    _, _, _, lddw, es = _batch("out", out, (dtype,))
+    _run(d, lib().moe_grouped_gemm_wgrad, dy.data_ptr(), lddy, x.data_ptr(), ldx, rows, off, E, N, K, out.data_ptr(), lddw, es,
+         dw_fp32, accumulate)
+    return out
 
 
 def moe_quantize_fp8(x: torch.Tensor, swiglu: bool = False):
     """(E4M3 codes uint8 [rows, K], fp32 scales [rows, ceil(K/128)]) of bf16 rows x [rows, K], or of
     silu(gate) * up of x [rows, 2K] with swiglu."""
-    _matrix("x", x, _BF16)
-    rows, K = x.shape
+    rows, K, ldx = _matrix("x", x, _BF16)
     if swiglu:
         if K % 2:
             raise ValueError("x: gate and up halves expected")
         K //= 2
     d = _device(x)
+    KB = -(-K // 128)
     device = x.device
-    codes = torch.empty((rows, K), dtype=torch.uint8, device=device)
-    scale = torch.empty((rows, -(-K // 128)), dtype=torch.float32, device=device)
-    _run(d, lib().moe_quantize_fp8, x.data_ptr(), _ld(x), rows, K, int(swiglu), codes.data_ptr(), K, scale.data_ptr())
+    codes = torch.empty_strided((rows, K), (K, 1), dtype=torch.uint8, device=device)
+    scale = torch.empty_strided((rows, KB), (KB, 1), dtype=torch.float32, device=device)
+    _run(d, lib().moe_quantize_fp8, x.data_ptr(), ldx, rows, K, swiglu, codes.data_ptr(), K, scale.data_ptr())
     return codes, scale
 
 
@@ -466,23 +476,21 @@ def moe_grouped_gemm_fp8(xq: torch.Tensor, xs: torch.Tensor, offsets: Optional[t
                          ws: torch.Tensor, y_fp32: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """moe_grouped_gemm of E4M3 operands with fp32 scales per 128 of K: xq [rows, K], xs
     [rows, ceil(K/128)], wq [E, N, K], ws [E, N, ceil(K/128)] (wq and ws without E with offsets None)."""
-    wq, ws = _experts_of(wq), _experts_of(ws)
-    _matrix("xq", xq, _FP8)
-    _matrix("wq", wq, _FP8, 3)
-    E, N, K = wq.shape
+    rows, cols, ldx = _matrix("xq", xq, _FP8)
+    E, N, K, ldw, es = _batch("wq", wq, _FP8)
     KB = -(-K // 128)
-    rows = xq.shape[0]
-    if xq.shape[1] != K:
-        raise ValueError(f"xq has {xq.shape[1]} columns, wq {K}")
-    if xs.dtype != torch.float32 or tuple(xs.shape) != (rows, KB) or not xs.is_contiguous():
+    if cols != K:
+        raise ValueError(f"xq has {cols} columns, wq {K}")
+    if xs.dtype != torch.float32 or xs.shape != (rows, KB) or not xs.is_contiguous():
         raise ValueError(f"xs: expected contiguous float32 [{rows}, {KB}]")
-    if ws.dtype != torch.float32 or tuple(ws.shape) != (E, N, KB) or (E > 0 and not ws[0].is_contiguous()):
+    sE, sN, sKB, lds, ses = _batch("ws", ws, (torch.float32,))
+    if (sE, sN, sKB) != (E, N, KB) or (lds != KB and N > 1):
         raise ValueError(f"ws: expected float32 [{E}, {N}, {KB}], dense per expert")
     off = _offsets(offsets, E)
     d = _device(xq, xs, offsets, wq, ws, out)
-    y = _result(out, (rows, N), y_fp32, xq.device)
-    _run(d, lib().moe_grouped_gemm_fp8, xq.data_ptr(), _ld(xq), xs.data_ptr(), rows, off, wq.data_ptr(), _ld(wq),
-         _estride(wq), ws.data_ptr(), _estride(ws), E, N, K, y.data_ptr(), _ld(y), int(y_fp32))
+    y, ldy = _result(out, rows, N, y_fp32, xq.device)
+    _run(d, lib().moe_grouped_gemm_fp8, xq.data_ptr(), ldx, xs.data_ptr(), rows, off, wq.data_ptr(), ldw, es, ws.data_ptr(), ses,
+         E, N, K, y.data_ptr(), ldy, y_fp32)
     return y
 
 

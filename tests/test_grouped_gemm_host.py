@@ -116,8 +116,10 @@ def test_the_binding_refuses_what_the_library_cannot_see():
             call()
     # one expert's weights seen as several have stride 0, which means "dense" to the library
     with pytest.raises(ValueError, match="expanded"):
-        moe._lib._estride(w[:1].expand(2, 32, 64))
-    assert moe._lib._ld(torch.zeros(1, 40, dtype=bf)) == 48         # a lone row's stride says nothing
+        moe.moe_grouped_gemm(x, off, w[:1].expand(2, 32, 64))
+    with pytest.raises(ValueError, match="expanded"):
+        moe.moe_grouped_gemm_fp8(q, s, off, wq, ws[:1].expand(2, 32, 2))
+    assert moe._lib._matrix("x", torch.zeros(1, 40, dtype=bf), (bf,)) == (1, 40, 48)   # a lone row's stride says nothing
 
 
 def test_the_abi_declares_them():
