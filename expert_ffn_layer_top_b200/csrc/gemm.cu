@@ -549,7 +549,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
         if (MODE != kGemmWgrad && BIG > kGemmBoxRows) tma_prefetch_desc(&bbig);
     }
     pdl_wait();
-    if (threadIdx.x == 0) pdl_release();
     int2 *range = const_cast<int2 *>(gemm_ranges(sm));
     int *tile_start = const_cast<int *>(gemm_tile_starts<BN>(sm, p));
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
@@ -558,8 +557,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
         range[e] = make_int2(beg, n);
     }
     __syncthreads();
-    // (after the wait: a kernel that held TMEM while it waits for one that still has to allocate
-    // its own on the same SM would never end)
+    // TMEM between the wait and the release: a kernel that holds some while it waits for another one
+    // that has yet to allocate its own on the same SM would never end
     if (warp == 2) gemm_tmem_alloc<CG>(&sm.tmem_base, TMEM_COLS);
     if (warp == 3) {   // first row tile of each expert
         int run = 0;
@@ -579,6 +578,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
     }
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0) pdl_release();
     if (CG == 2) cluster_sync_all();   // the peer's barriers exist before anything arrives on them
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
