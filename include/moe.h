@@ -3,7 +3,8 @@
  *
  * One hot path: the forward pass of a mixture-of-experts layer over
  * quantised experts, plus the device expert cache that lets an expert pool
- * larger than device memory stream from pinned host memory.
+ * larger than device memory stream from pinned host memory. Its products by
+ * expert are available by themselves too, with their gradients.
  *
  * Sources. The pages describing the serving engine this layer comes from give
  * the problem, not the kernels:
