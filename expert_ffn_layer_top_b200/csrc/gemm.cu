@@ -1045,22 +1045,49 @@ static moe_status gemm_launch(const GemmArgs &a, int nsm, cudaStream_t st) {
     return e == cudaSuccess ? MOE_OK : set_cuda_error(e, "grouped product launch");
 }
 
-// Tiles of up to 64 rows on single CTAs where experts have up to 48 rows on average, else pairs
-// of CTAs (256 m's) with tiles of up to BN rows. The products of few rows are bound by reading
-// the weights, which single CTAs with more stages do a little faster (E = 32, K = 2048, N = 1536,
-// 16 rows each: 40.9 against 42.4 us, fp8 24.7 against 32.2); with more rows the small tile has
-// to read them, and the rows, again and again (64 rows: 45.8 against 46.8 us, fp8 35.9 against
-// 41.0; 128 rows: 76 against 49 us, fp8 59 against 48).
+// Rounds over the SMs that tiles of BN rows take. The row ranges are on the device, so the tiles are
+// estimated: half a tile per expert more than its rows fill, and one at least.
+static double gemm_rounds(const GemmArgs &a, int M, int nsm, int CG, int BN) {
+    const double e = std::max(1, std::min(a.E, a.n_rows));
+    const double tiles = e * std::max(1.0, a.n_rows / (e * BN) + 0.5);
+    return tiles * ((M + 128 * CG - 1) / (128 * CG)) / (gemm_ctas(BN) * nsm / CG);
+}
+// Their time where a whole round takes `round`: the mean of 10% fewer and 15% more tiles' rounds.
+static double gemm_time(double rounds, double round) {
+    return 0.5 * (std::ceil(0.9 * rounds) + std::ceil(1.15 * rounds)) * round;
+}
+
+// Up to 8 rounds of pairs, the tile that needs the least time in whole rounds. A round's time, in that
+// of pairs, was measured at K = 2048 (tiles of 32, 64, 128 rows and pairs: 10.3, 11, 12 and 15 us;
+// fp8 11.2, 7.5, 11.6 and 14; with one CTA an SM at most, fp8 tiles of 32 are the quickest of all).
+// Against a choice by the mean of an expert's rows alone (up to 24, 48 or more): 9% less on average over
+// 693 sizes, 2% above the best tile of each; 8 experts of 64 rows, K = 2048, N = 512: 18.0 -> 13.5 us;
+// N = 2048: 18.7 -> 16.7; 40 experts of 32 rows, N = 512: 24.5 -> 17.7.
+// Beyond, reading the weights bounds the products of few rows, and a tile should hold an expert's
+// rows so that they are read once: tiles of 32 or 64 rows where experts have up to 24 or 48 (fp8: 80)
+// on average (128 experts, N = K = 2048, 64 rows: 208 us with tiles of 64, 194 with pairs; fp8 140 and 144).
 // More than kGemmStrip tiles of 256 m's (M > 4096): in strips (8192^3: 715 against 775 us; with
 // fewer, where they would only change the order within an expert, the kernels without the
 // divisions are 1 to 2% faster).
 template <int MODE, int BN>
 static moe_status gemm_pick(const GemmArgs &a, int nsm, cudaStream_t st) {
-    if constexpr (MODE != kGemmWgrad)
-        if (a.n_rows <= 24 * (int64_t)a.E) return gemm_launch<MODE, 1, 32>(a, nsm, st);
-    if constexpr (MODE != kGemmWgrad)
-        if (a.n_rows <= 48 * (int64_t)a.E) return gemm_launch<MODE, 1, 64>(a, nsm, st);
     const int M = MODE == kGemmWgrad || MODE == kGemmDgrad ? a.K : a.N;
+    if constexpr (MODE != kGemmWgrad) {
+        constexpr bool FP8 = MODE == kGemmFp8;
+        const double pairs = gemm_time(gemm_rounds(a, M, nsm, 2, BN), 1.0);
+        int bn = a.n_rows <= 24 * (int64_t)a.E ? 32 : a.n_rows <= (FP8 ? 80 : 48) * (int64_t)a.E ? 64 : BN;
+        if (pairs <= 8) {
+            const double rounds = gemm_rounds(a, M, nsm, 1, 32);
+            const double t32 = FP8 && rounds <= 0.5 ? 0.58 : gemm_time(rounds, FP8 ? 0.85 : 0.69);
+            const double t64 = gemm_time(gemm_rounds(a, M, nsm, 1, 64), FP8 ? 0.6 : 0.75);
+            const double t128 = gemm_time(gemm_rounds(a, M, nsm, 1, 128), 0.85);
+            const double least = std::min(std::min(t32, t64), std::min(t128, pairs));
+            bn = least == t32 ? 32 : least == t64 ? 64 : least == t128 ? 128 : BN;
+        }
+        if (bn == 32) return gemm_launch<MODE, 1, 32>(a, nsm, st);
+        if (bn == 64) return gemm_launch<MODE, 1, 64>(a, nsm, st);
+        if (bn == 128) return gemm_launch<MODE, 1, 128>(a, nsm, st);
+    }
     if (M > kGemmStrip * 256) return gemm_launch<MODE, 2, BN, true>(a, nsm, st);
     return gemm_launch<MODE, 2, BN>(a, nsm, st);
 }

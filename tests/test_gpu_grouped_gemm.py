@@ -189,12 +189,14 @@ def _within(got, want64, terms, S, extra=0.0):
 
 
 COUNTS = [70, 0, 1, 300, 22]
+MANY = [300, 301, 255, 0, 513, 100, 1, 700]   # rows that CTA pairs take
 
 
+@pytest.mark.parametrize("COUNTS,K,N", [(COUNTS, 600, 328), (MANY, 1160, 2056), (MANY, 2056, 1160), ([1300], 600, 1000)])
 @pytest.mark.parametrize("fp32", [False, True])
-def test_random_values_stay_within_the_bound(moe, fp32):
+def test_random_values_stay_within_the_bound(moe, fp32, COUNTS, K, N):
     g = _gen(6)
-    K, N, R, E = 600, 328, sum(COUNTS), len(COUNTS)
+    R, E = sum(COUNTS), len(COUNTS)
     x = torch.randn(R, K, generator=g, device="cuda").to(BF16)
     dy = torch.randn(R, N, generator=g, device="cuda").to(BF16)
     w = (torch.randn(E, N, K, generator=g, device="cuda") * 0.02).to(BF16)
@@ -206,11 +208,11 @@ def test_random_values_stay_within_the_bound(moe, fp32):
             _wgrad64(dy.abs(), x.abs(), COUNTS))
 
 
-@pytest.mark.parametrize("K", [640, 2000])
+@pytest.mark.parametrize("COUNTS,K,N", [(COUNTS, 640, 328), (COUNTS, 2000, 328), (MANY, 2000, 2056), ([1300], 640, 1000)])
 @pytest.mark.parametrize("fp32", [False, True])
-def test_fp8_random_values_stay_within_the_bound(moe, fp32, K):
+def test_fp8_random_values_stay_within_the_bound(moe, fp32, COUNTS, K, N):
     g = _gen(7)
-    N, R, E = 328, sum(COUNTS), len(COUNTS)
+    R, E = sum(COUNTS), len(COUNTS)
     xq, xs = moe.moe_quantize_fp8(torch.randn(R, K, generator=g, device="cuda").to(BF16))
     wq, ws = moe.moe_quantize_fp8((torch.randn(E * N, K, generator=g, device="cuda") * 0.02).to(BF16))
     wq, ws = wq.view(E, N, K), ws.view(E, N, -1)
@@ -350,6 +352,64 @@ def test_a_row_and_an_expert_keep_their_values_to_themselves(moe, bad):
     got = moe.moe_grouped_gemm_fp8(xq, xs, off, wq, ws, y_fp32=True)
     assert torch.equal(got[keep], want[keep])
     assert torch.isnan(got[50]).all() and torch.isnan(got[mid]).all() and not torch.isfinite(got[51]).any()
+
+
+# rows per expert and output columns that take each of the tiles (bf16; fp8): of 64; 32, 64; 128, 64;
+# 128, 64; pairs; pairs; pairs; 128, 128
+TILES = [
+    ([40, 0, 33, 70, 12] * 30, 1160), ([45] * 40, 2056), ([64, 100, 128, 60, 90, 70, 110, 33], 2056),
+    ([80, 64, 65, 0, 129, 63] * 4, 2056), (MANY, 2056), ([1100, 257, 3, 0] * 3, 2056), ([2500], 1160), ([1300], 1000),
+]
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("counts,cols", TILES)
+def test_every_tile_keeps_to_its_rows(moe, counts, cols, fp32):
+    """Exact results from strided operands; rows before the first expert and behind the last hold NaN and
+    stay as they were; one expert's rows and weights are NaN, and one row of another."""
+    g = _gen(23)
+    E, R, before, after, C = len(counts), sum(counts), 5, 11, 272
+    n = before + R + after
+    off = _offsets(counts, before)
+    rows = slice(before, before + R)
+    nan = float("nan")
+    at = np.concatenate([[0], np.cumsum(counts)])
+    keep = torch.ones(R, dtype=torch.bool, device="cuda")
+    lone = int(at[E // 2]) if E > 1 else 700     # a row that is NaN by itself
+    keep[lone] = False
+    bad = max(e for e in range(E) if counts[e] and e != E // 2) if E > 1 else None
+    if bad is not None:
+        keep[at[bad]:at[bad + 1]] = False
+
+    def check(call, want):
+        big = torch.full((n, cols + 8), 7.0, dtype=torch.float32 if fp32 else BF16, device="cuda")
+        got = call(big[:, :cols])[rows]
+        _same(got[keep], want[keep], fp32)
+        assert torch.isnan(got[~keep]).all()
+        big[rows, :cols] = 7.0
+        assert (big == 7.0).all()
+
+    x = torch.full((n, C), nan, dtype=BF16, device="cuda")
+    x[rows] = _ints(g, R, C)
+    x[rows][~keep] = nan
+    x = _strided(x, 8, nan)
+    w = _ints(g, E, cols, C)
+    if bad is not None:
+        w[bad] = nan
+    wt = _strided(w.transpose(1, 2).contiguous(), 8, nan)
+    w = _strided(w, 8, nan)
+    want = _forward64(x[rows], counts, w)
+    check(lambda o: moe.moe_grouped_gemm(x, off, w, y_fp32=fp32, out=o), want)
+    check(lambda o: moe.moe_grouped_gemm_dgrad(x, off, wt, dx_fp32=fp32, out=o), want)
+    xq, xs, xf = _fp8_ints(g, n, C)
+    wq, ws, wf = _fp8_ints(g, E, cols, C)
+    want = _forward64(xf[rows], counts, wf)
+    xq[rows][~keep] = 0x7F
+    xq[:before], xs[before + R:] = 0x7F, nan
+    if bad is not None:
+        ws[bad] = nan
+    check(lambda o: moe.moe_grouped_gemm_fp8(_strided(xq, 16, 0x7F), xs, off, _strided(wq, 16, 0x7F), ws, y_fp32=fp32, out=o),
+          want)
 
 
 def test_empty_batches(moe):
