@@ -412,6 +412,43 @@ def test_every_tile_keeps_to_its_rows(moe, counts, cols, fp32):
           want)
 
 
+# tiles of 64 columns, 64, 128, 128, pairs, pairs
+WGRAD_TILES = [
+    ([1, 17, 0, 63, 130], 200, 264), ([700, 4300], 512, 264), ([100, 64, 65, 0, 128, 129, 1, 112], 512, 1160), ([2500], 1160, 1160),
+    (MANY, 2056, 1160), ([1300, 0, 1101], 2056, 1160),
+]
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("counts,N,K", WGRAD_TILES)
+def test_every_tile_of_weight_gradients_keeps_to_its_expert(moe, counts, N, K, fp32):
+    """Exact from strided operands, added to what is there or not; the rows around the experts hold NaN,
+    and one expert's rows too."""
+    g = _gen(24)
+    E, R, before, after = len(counts), sum(counts), 3, 11
+    off = _offsets(counts, before)
+    rows = slice(before, before + R)
+    x = torch.full((before + R + after, K), float("nan"), dtype=BF16, device="cuda")
+    dy = torch.full((before + R + after, N), float("nan"), dtype=BF16, device="cuda")
+    x[rows], dy[rows] = _ints(g, R, K), _ints(g, R, N)
+    keep = torch.ones(E, dtype=torch.bool, device="cuda")
+    if E > 1:
+        keep[1] = False
+        x[rows][counts[0]:counts[0] + counts[1]] = float("nan")
+    x, dy = _strided(x, 8, float("nan")), _strided(dy, 16, float("nan"))
+    want = _wgrad64(dy[rows], x[rows], counts)
+    big = torch.full((E, N, K + 8), 7.0, dtype=torch.float32 if fp32 else BF16, device="cuda")
+    out = big[..., :K]
+    assert moe.moe_grouped_gemm_wgrad(dy, x, off, dw_fp32=fp32, out=out) is out
+    _same(out[keep], want[keep], fp32)
+    if E > 1:
+        assert torch.isnan(out[1]).all() or counts[1] == 0
+    if fp32:
+        moe.moe_grouped_gemm_wgrad(dy, x, off, out=out, accumulate=True)
+        _same(out[keep], 2 * want[keep], fp32)
+    assert (big[..., K:] == 7.0).all()
+
+
 def test_empty_batches(moe):
     off = torch.zeros(4, dtype=torch.int32, device="cuda")
     w = _ints(_gen(10), 3, 64, 72)
