@@ -77,12 +77,12 @@ def _same(got, want64, fp32):
 
 
 # rows per expert, K, N: one token, empty experts, tiles that end inside, one under and one over a
-# tile, sizes that no tile divides, K and N below one tile
+# tile, sizes that no tile divides, K and N below one tile, sums of more than one part of 8192
 SHAPES = [
     ([1], 64, 128), ([1], 8, 8), ([3, 0, 1], 2048, 256), ([0, 0, 5, 0], 128, 520), ([16, 17, 15], 264, 136),
     ([255, 256, 257], 128, 256), ([511, 1, 513, 0, 31], 192, 384), ([1300], 512, 1000), ([64] * 9, 768, 264),
     ([2, 1] * 40, 256, 512), ([33, 700, 129, 5], 1000, 1160), ([8] * 200, 72, 40), ([30] * 6, 200, 264),
-    ([1, 0, 2] * 300, 64, 72),
+    ([1, 0, 2] * 300, 64, 72), ([9, 40], 8264, 72), ([3, 9], 72, 8264), ([8300, 16500], 72, 136),
 ]
 
 
