@@ -521,6 +521,7 @@ int cache_layout(const struct expert_cache *c);
 // ------------------------------------------------------------------ checks of the grouped products
 
 constexpr int kMaxProductDim = 1 << 24;
+constexpr int64_t kMaxRowStride = (int64_t)1 << 36;   // products of strides and extents stay within 64 bits
 
 static moe_status check_product(int E, int N, int K, int n_rows, const int32_t *offsets) {
     if (E < 1 || E > kMaxExperts) return set_error(MOE_ERR_UNSUPPORTED, "E=%d outside 1..%d", E, kMaxExperts);
@@ -537,7 +538,7 @@ static moe_status check_product(int E, int N, int K, int n_rows, const int32_t *
 static moe_status check_operand(const char *what, const void *p, int64_t cols, int64_t ld, int esz) {
     if (!p) return set_error(MOE_ERR_INVALID_ARG, "%s is NULL", what);
     if (misaligned(p, 16)) return set_error(MOE_ERR_INVALID_ARG, "%s must be 16-byte aligned", what);
-    if (ld < cols || ld * esz % 16 || ld > (int64_t)1 << 36)
+    if (ld < cols || ld % (16 / esz) || ld > kMaxRowStride)
         return set_error(MOE_ERR_INVALID_ARG, "%s: row stride %lld must be at least %lld and a multiple of 16 bytes",
                          what, (long long)ld, (long long)cols);
     return MOE_OK;
@@ -555,7 +556,8 @@ static moe_status check_estride(int64_t *estride, int E, int64_t rows, int64_t c
 static moe_status check_result(const void *p, int64_t cols, int64_t ld, int fp32) {
     if (!p) return set_error(MOE_ERR_INVALID_ARG, "the result is NULL");
     if (misaligned(p, fp32 ? 4 : 2)) return set_error(MOE_ERR_INVALID_ARG, "the result must be aligned to its elements");
-    if (ld < cols) return set_error(MOE_ERR_INVALID_ARG, "result: row stride %lld below %lld", (long long)ld, (long long)cols);
+    if (ld < cols || ld > kMaxRowStride)
+        return set_error(MOE_ERR_INVALID_ARG, "result: row stride %lld below %lld or too large", (long long)ld, (long long)cols);
     return MOE_OK;
 }
 
@@ -754,7 +756,7 @@ moe_status moe_quantize_fp8(const void *x, int64_t ldx, int rows, int K, int swi
     if (rows == 0) return MOE_OK;
     if (!x || !codes || !scale) return set_error(MOE_ERR_INVALID_ARG, "NULL pointer");
     const int64_t width = swiglu ? 2 * (int64_t)K : K;
-    if (ldx < width || ldx % 8 || ldc < K || ldc % 16)
+    if (ldx < width || ldx % 8 || ldx > kMaxRowStride || ldc < K || ldc % 16 || ldc > kMaxRowStride)
         return set_error(MOE_ERR_INVALID_ARG, "ldx=%lld and ldc=%lld must hold a row and be multiples of 8 and 16",
                          (long long)ldx, (long long)ldc);
     if (misaligned(x, 16) || misaligned(codes, 16) || misaligned(scale, 4))

@@ -286,7 +286,8 @@ moe_status moe_dequantize(int fmt, const void *w, const void *scale, float tscal
  *   - No workspace and no synchronisation; calls can be captured into graphs.
  *   Errors: UNSUPPORTED for E outside 1..1024, N or K above 2^24 or n_rows above
  *   2^30; INVALID_ARG for N, K or n_rows below their range, NULL pointers,
- *   misaligned ones, or strides that break the rules above. */
+ *   misaligned ones, strides that break the rules above, or rows more than 2^36
+ *   elements apart. */
 
 /* y[r][n] = sum_k x[r][k] w[e][n][k].
  *   x: bf16 [n_rows][K]; w: bf16 [E][N][K]; y: [n_rows][N], bf16, or fp32 if y_is_fp32. */

@@ -42,6 +42,8 @@ def test_products_check_their_arguments(name):
     assert g(we=256 * 255) == INVALID_ARG and g(we=256 * 256 + 4) == INVALID_ARG
     assert g(ldy=255) == INVALID_ARG
     assert g(y=A + 1) == INVALID_ARG and g(y=A + 2, fp32=1) == INVALID_ARG
+    for ld in ("ldx", "ldw", "ldy"):                               # no product of strides leaves 64 bits
+        assert g(**{ld: 1 << 60}) == INVALID_ARG and g(**{ld: (1 << 63) - 16}) == INVALID_ARG
 
 
 def test_wgrad_checks_its_arguments():
@@ -55,6 +57,7 @@ def test_wgrad_checks_its_arguments():
         assert g(**{p: None}) == INVALID_ARG
     assert g(dy=A + 2) == INVALID_ARG and g(lddy=260) == INVALID_ARG and g(ldx=128) == INVALID_ARG
     assert g(ld=255) == INVALID_ARG and g(es=256 * 255) == INVALID_ARG and g(dw=A + 2) == INVALID_ARG
+    assert g(ld=1 << 60) == INVALID_ARG and g(lddy=1 << 62) == INVALID_ARG and g(es=1 << 62) == INVALID_ARG
 
 
 def test_fp8_product_checks_its_arguments():
@@ -81,6 +84,7 @@ def test_quantiser_checks_its_arguments():
     for p in ("x", "codes", "scale"):
         assert q(**{p: None}) == INVALID_ARG
     assert q(ldx=252) == INVALID_ARG and q(ldx=260) == INVALID_ARG and q(ldc=264) == INVALID_ARG
+    assert q(ldx=1 << 60) == INVALID_ARG and q(ldc=1 << 60) == INVALID_ARG
     assert q(sw=1) == INVALID_ARG                                   # gate and up need 512 columns
     assert q(x=A + 8) == INVALID_ARG and q(codes=A + 8) == INVALID_ARG and q(scale=A + 2) == INVALID_ARG
 
