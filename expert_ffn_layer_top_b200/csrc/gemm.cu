@@ -1253,7 +1253,9 @@ __global__ void __launch_bounds__(256) quantize_fp8_kernel(const __nv_bfloat16 *
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = quotient(v[j], s, r);
             } else {
-                s = top == 0 ? 1.0f : __fdiv_rn(amax, 448.0f);
+                // 0 from amax = 0, and with SwiGLU from an amax up to 224 * 2^-149: 1 then, for 0 / 0 is NaN
+                s = __fdiv_rn(amax, 448.0f);
+                if (s == 0.0f) s = 1.0f;
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = __fdiv_rn(v[j], s);
             }

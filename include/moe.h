@@ -312,7 +312,8 @@ moe_status moe_grouped_gemm_wgrad(const void *dy, int64_t lddy, const void *x, i
                                   int64_t dw_estride, int dw_is_fp32, int accumulate, moe_stream_t stream);
 
 /* Activations into the FP8 expert format: per row and 128-wide block of K (the
- * last one may be shorter) s = amax / 448, or 1 where amax is 0, and codes
+ * last one may be shorter) s = amax / 448, or 1 where that is 0 (an amax of 0, or
+ * with swiglu one up to 224 * 2^-149), and codes
  * E4M3(v / s), to nearest, ties to even, saturating; each step is one correctly
  * rounded fp32 operation. A block that holds an infinity or a NaN decodes to NaN
  * throughout.

@@ -1,0 +1,43 @@
+"""Edges of the grouped products and of the FP8 quantiser: values next to fp32's smallest."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def moe():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    import expert_ffn_layer_top_b200 as m
+
+    yield m
+    assert m.moe_device_error() == 0
+
+
+# ---------------------------------------------------------------------------- quantiser
+
+
+@pytest.mark.parametrize("units", [1, 3, 223, 224, 225, 255])
+@pytest.mark.parametrize("K", [256, 144])
+def test_swiglu_blocks_next_to_the_smallest_value_stay_finite(moe, K, units):
+    """silu(2^-70) = 2^-71 in fp32, so the largest value of the last block is units * 2^-149. units / 448
+    rounds to 0 up to 224 (a tie at one half goes to even) and to one unit beyond."""
+    x = torch.zeros(3, 2 * K, dtype=BF16)
+    at = K - 7
+    x[0, at], x[0, K + at] = 2.0**-70, units * 2.0**-78
+    x[1, at], x[1, K + at] = 2.0**-70, -units * 2.0**-78
+    x[2, at], x[2, K + at] = 1e-22, 1e-21
+    codes, scale = moe.moe_quantize_fp8(x.cuda(), swiglu=True)
+    values = codes.cpu().view(torch.float8_e4m3fn).float()
+    want = torch.ones(3, 2)
+    code = torch.zeros(3, K)
+    if units > 224:
+        want[:2, 1] = 2.0**-149
+        code[0, at] = 224.0 if units == 225 else 256.0     # steps of 16 below 256
+        code[1, at] = -code[0, at]
+    assert torch.equal(scale.cpu(), want) and torch.equal(values, code)
+    w = torch.ones(8, K, dtype=torch.float8_e4m3fn, device="cuda")
+    y = moe.moe_grouped_gemm_fp8(codes, scale, None, w, torch.ones(8, 2, device="cuda"), y_fp32=True)
+    assert torch.equal(y.cpu(), (code.sum(1) * want[:, 1])[:, None].expand(3, 8))
