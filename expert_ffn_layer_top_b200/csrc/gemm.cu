@@ -1150,16 +1150,19 @@ moe_status launch_grouped_gemm(const GemmArgs &a, int nsm, cudaStream_t st) {
 // ------------------------------------------------------------------ FP8 quantiser
 // Bound by memory (3.03 bytes an element, 5.03 with SwiGLU) once the arithmetic per element is
 // short: 16 elements a lane, so that a block's scale and addresses are worked out by 8 lanes
-// and not by 16, maxima on pairs of bf16 and quotients by a reciprocal. The codes and scales
-// are those of correctly rounded fp32 operations bit for bit.
+// and not by 16, maxima on pairs of bf16 and quotients by a reciprocal. Scales and codes are
+// those of correctly rounded fp32 divisions of the values bit for bit; with SwiGLU the values
+// themselves go through expf and an approximate division, a few units in the last place off
+// (more for gates below -87, where exp(gate) is below fp32's normal numbers).
 
 constexpr int kQuantAhead = 2;   // blocks of a lane group whose loads are under way at a time
 
 // RN(v / s) from r = RN(1 / s): Markstein's method (IBM J. Res. Dev. 34, 1990), exact while
-// nothing over- or underflows on the way.
+// nothing over- or underflows on the way. The remainder is taken with its sign turned, so that
+// the quotient of -0 is -0: v - q s would be +0 there, and +0 + -0 is +0.
 __device__ __forceinline__ float quotient(float v, float s, float r) {
     const float q = __fmul_rn(v, r);
-    return __fmaf_rn(__fmaf_rn(-q, s, v), r, q);
+    return __fmaf_rn(-__fmaf_rn(q, s, -v), r, q);
 }
 
 __device__ __forceinline__ uint32_t e4m3x4_code(float a, float b, float c, float d) {

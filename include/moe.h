@@ -314,12 +314,14 @@ moe_status moe_grouped_gemm_wgrad(const void *dy, int64_t lddy, const void *x, i
 /* Activations into the FP8 expert format: per row and 128-wide block of K (the
  * last one may be shorter) s = amax / 448, or 1 where that is 0 (an amax of 0, or
  * with swiglu one up to 224 * 2^-149), and codes
- * E4M3(v / s), to nearest, ties to even, saturating; each step is one correctly
- * rounded fp32 operation. A block that holds an infinity or a NaN decodes to NaN
- * throughout.
+ * E4M3(v / s), to nearest, ties to even, saturating; both divisions are correctly
+ * rounded fp32 ones, and a zero keeps its sign. A block that holds an infinity or
+ * a NaN decodes to NaN throughout.
  *   swiglu 0: v = x[r][k], x bf16 [rows][K].
  *   swiglu 1: v = silu(x[r][k]) * x[r][K + k] in fp32, x bf16 [rows][2K], the
- *     rows that moe_grouped_gemm(_fp8) makes with w13 (gate, then up).
+ *     rows that moe_grouped_gemm(_fp8) makes with w13 (gate, then up). silu is off
+ *     by a few units in the last place for gates above -87; below, where
+ *     exp(gate) leaves fp32's normal numbers, by more, and it is -0 from -104 on.
  *   codes: E4M3 bytes [rows][K], ldc bytes a row; scale: fp32 [rows][ceil(K/128)],
  *   dense. moe_dequantize(MOE_FP8_E4M3_K128) reads dense results back (K % 128 == 0,
  *   finite blocks, scales below 128).

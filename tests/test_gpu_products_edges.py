@@ -1,4 +1,4 @@
-"""Edges of the grouped products and of the FP8 quantiser: values next to fp32's smallest."""
+"""Edges of the grouped products and of the FP8 quantiser: values next to fp32's smallest, signed zeros."""
 import pytest
 import torch
 
@@ -41,3 +41,31 @@ def test_swiglu_blocks_next_to_the_smallest_value_stay_finite(moe, K, units):
     w = torch.ones(8, K, dtype=torch.float8_e4m3fn, device="cuda")
     y = moe.moe_grouped_gemm_fp8(codes, scale, None, w, torch.ones(8, 2, device="cuda"), y_fp32=True)
     assert torch.equal(y.cpu(), (code.sum(1) * want[:, 1])[:, None].expand(3, 8))
+
+
+@pytest.mark.parametrize("rows,K", [(3, 144), (40, 1024)])
+def test_signs_of_zeros_are_those_of_the_division(moe, rows, K):
+    g = torch.Generator().manual_seed(rows)
+    x = torch.randn(rows, K, generator=g).to(BF16)
+    zeros = torch.rand(rows, K, generator=g)
+    x[zeros < 0.2] = 0.0
+    x[zeros > 0.8] = -0.0
+    x[0, :128] = -0.0
+    x[1, 5] = -(2.0**-60)                # a code of 0 from a value that is not
+    codes, scale = moe.moe_quantize_fp8(x.cuda())
+    blk = torch.nn.functional.pad(x.float(), (0, -K % 128)).view(rows, -1, 128)
+    amax = blk.abs().amax(-1)
+    s = torch.where(amax == 0, torch.ones_like(amax), amax / 448.0)
+    q = (blk / s.unsqueeze(-1)).to(torch.float8_e4m3fn).view(rows, -1)[:, :K]
+    assert torch.equal(scale.cpu(), s) and torch.equal(codes.cpu(), q.contiguous().view(torch.uint8))
+
+
+def test_swiglu_keeps_the_sign_of_zeros(moe):
+    """silu of a far negative gate is -0."""
+    x = torch.ones(2, 256, dtype=BF16)
+    x[:, 3] = -200.0
+    x[0, 7], x[0, 128 + 7] = 0.0, -1.0
+    x[1, 128 + 3] = -1.0
+    codes, _ = moe.moe_quantize_fp8(x.cuda(), swiglu=True)
+    codes = codes.cpu()
+    assert codes[0, 3] == 0x80 and codes[1, 3] == 0x00 and codes[0, 7] == 0x80
