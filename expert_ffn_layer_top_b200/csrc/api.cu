@@ -719,6 +719,7 @@ moe_status moe_grouped_gemm_wgrad(const void *dy, int64_t lddy, const void *x, i
     if (accumulate && !dw_is_fp32) return set_error(MOE_ERR_UNSUPPORTED, "dw is accumulated in fp32 only");
     if ((r = check_result(dw, K, lddw, dw_is_fp32)) != MOE_OK) return r;
     if ((r = check_estride(&dw_estride, E, N, K, lddw, 1)) != MOE_OK) return r;
+    if (n_rows == 0 && accumulate) return MOE_OK;
     if (n_rows == 0) {   // no operand is read: any aligned address describes it
         x = dy = reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(dw) & ~uintptr_t(15));
         ldx = (int64_t)align_up(K, 8);

@@ -893,6 +893,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &amap, const CUtenso
             const int part = p.part;
             for (int item = first; item < total && ok; item += step) {
                 const GemmItem it = gemm_item<MODE, CG, BN, STRIPS>(sm, p, item);
+                if (MODE == kGemmWgrad && p.accumulate && !it.kblocks) continue;   // nothing to add: dw is not touched
                 const int m = it.m0 + (int)rank * 128 + q * 32 + lane;
                 const int jn = MODE == kGemmWgrad ? min(it.nt, p.J - it.j0) : it.valid;   // columns to store
                 const int units = (it.nt / 16 + G - 1 - g) / G;

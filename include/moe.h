@@ -306,7 +306,7 @@ moe_status moe_grouped_gemm_dgrad(const void *dy, int64_t lddy, int n_rows, cons
  * an expert without rows.
  *   dy: bf16 [n_rows][N]; x: bf16 [n_rows][K]; dw: [E][N][K], fp32 if dw_is_fp32,
  *   else bf16. accumulate: add to what dw holds, in fp32 (UNSUPPORTED for bf16);
- *   an expert without rows then keeps its values. */
+ *   an expert without rows then keeps its values, which are not read. */
 moe_status moe_grouped_gemm_wgrad(const void *dy, int64_t lddy, const void *x, int64_t ldx, int n_rows,
                                   const int32_t *offsets, int E, int N, int K, void *dw, int64_t lddw,
                                   int64_t dw_estride, int dw_is_fp32, int accumulate, moe_stream_t stream);

@@ -1,4 +1,5 @@
-"""Edges of the grouped products and of the FP8 quantiser: values next to fp32's smallest, signed zeros."""
+"""Edges of the grouped products and of the FP8 quantiser: values next to fp32's smallest, signed zeros, experts
+without rows."""
 import pytest
 import torch
 
@@ -14,6 +15,14 @@ def moe():
 
     yield m
     assert m.moe_device_error() == 0
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _offsets(counts):
+    return torch.tensor([0] + list(counts), device="cuda").cumsum(0).int()
 
 
 # ---------------------------------------------------------------------------- quantiser
@@ -69,3 +78,30 @@ def test_swiglu_keeps_the_sign_of_zeros(moe):
     codes, _ = moe.moe_quantize_fp8(x.cuda(), swiglu=True)
     codes = codes.cpu()
     assert codes[0, 3] == 0x80 and codes[1, 3] == 0x00 and codes[0, 7] == 0x80
+
+
+# ---------------------------------------------------------------------------- weight gradients
+
+
+@pytest.mark.parametrize("counts,N,K", [([0, 5, 0, 70], 136, 72), ([0, 900, 0, 1100, 0, 0, 700, 0], 2056, 1160),
+                                        ([0, 0, 0], 64, 200)])
+def test_accumulating_leaves_experts_without_rows_as_they_are(moe, counts, N, K):
+    g = _gen(1)
+    E, R = len(counts), sum(counts)
+    dy = torch.randint(-3, 4, (R, N), generator=g, device="cuda").to(BF16)
+    x = torch.randint(-3, 4, (R, K), generator=g, device="cuda").to(BF16)
+    dw = torch.randint(-9, 10, (E, N, K), generator=g, device="cuda").float()
+    dw[dw == 0] = -0.0
+    before = dw.clone()
+    launches = moe.lib().moe_kernel_launch_count()
+    moe.moe_grouped_gemm_wgrad(dy, x, _offsets(counts), out=dw, accumulate=True)
+    if R == 0:
+        assert moe.lib().moe_kernel_launch_count() == launches
+    at = 0
+    for e, n in enumerate(counts):
+        if n == 0:
+            assert torch.equal(dw[e].view(torch.int32), before[e].view(torch.int32))
+        else:
+            want = before[e].double() + dy[at:at + n].double().T @ x[at:at + n].double()
+            assert torch.equal(dw[e].double(), want)
+        at += n

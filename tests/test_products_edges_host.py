@@ -1,0 +1,22 @@
+"""What the grouped products answer or refuse before any device work, at their edges.
+
+The C calls get never-dereferenced pointers, so the module runs only where no device is visible."""
+import pytest
+import torch
+
+import expert_ffn_layer_top_b200 as moe
+
+pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="host-only checks; run where no device is visible")
+
+OK, INVALID_ARG, UNSUPPORTED = 0, 1, 2
+A = 1 << 24          # an aligned address that nothing reads
+
+
+def test_accumulating_no_rows_launches_nothing():
+    def g(dw=A, ld=256, dy=None, x=None, fp32=1, acc=1):
+        return moe.lib().moe_grouped_gemm_wgrad(dy, 256, x, 256, 0, A, 8, 256, 256, dw, ld, 0, fp32, acc, None)
+
+    before = moe.lib().moe_kernel_launch_count()
+    assert g() == OK and g(dy=A, x=A) == OK
+    assert moe.lib().moe_kernel_launch_count() == before
+    assert g(dw=None) == INVALID_ARG and g(ld=255) == INVALID_ARG and g(fp32=0) == UNSUPPORTED   # still checked
