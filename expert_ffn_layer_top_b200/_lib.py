@@ -322,6 +322,9 @@ _FP8 = (torch.uint8, torch.float8_e4m3fn)
 _BF16 = (torch.bfloat16,)
 
 
+_INT_MAX = 2**31 - 1   # sizes are C ints, which ctypes fills with a larger number's low bits
+
+
 # The wrappers below are called for every projection of a decode step, where their own time is
 # most of a small product's: each tensor's shape and strides are asked for once.
 
@@ -349,7 +352,8 @@ def _run(d: int, fn, *args):
 
 
 def _refuse(name: str, t: torch.Tensor, dtypes, ndim: int):
-    raise ValueError(f"{name}: expected {ndim}-D {' or '.join(str(d) for d in dtypes)} with a contiguous last dimension, "
+    raise ValueError(f"{name}: expected {ndim}-D {' or '.join(str(d) for d in dtypes)} with a contiguous last dimension "
+                     f"and sizes below 2^31, "
                      f"got {t.dtype} of shape {tuple(t.shape)} and strides {t.stride()}")
 
 
@@ -359,7 +363,7 @@ def _matrix(name: str, t: torch.Tensor, dtypes):
         _refuse(name, t, dtypes, 2)
     rows, cols = t.shape
     ld, unit = t.stride()
-    if unit != 1 and cols > 1:
+    if unit != 1 and cols > 1 or rows > _INT_MAX or cols > _INT_MAX:
         _refuse(name, t, dtypes, 2)
     return rows, cols, ld if rows > 1 else -(-cols // 16) * 16
 
@@ -372,7 +376,7 @@ def _batch(name: str, t: torch.Tensor, dtypes):
         _refuse(name, t, dtypes, 3)
     E, rows, cols = t.shape
     es, ld, unit = t.stride()
-    if unit != 1 and cols > 1:
+    if unit != 1 and cols > 1 or E > _INT_MAX or rows > _INT_MAX or cols > _INT_MAX:
         _refuse(name, t, dtypes, 3)
     if E <= 1:
         es = 0

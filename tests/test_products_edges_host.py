@@ -20,3 +20,27 @@ def test_accumulating_no_rows_launches_nothing():
     assert g() == OK and g(dy=A, x=A) == OK
     assert moe.lib().moe_kernel_launch_count() == before
     assert g(dw=None) == INVALID_ARG and g(ld=255) == INVALID_ARG and g(fp32=0) == UNSUPPORTED   # still checked
+
+
+def test_the_binding_refuses_sizes_that_leave_32_bits():
+    """Their low bits would name other, smaller sizes. Meta tensors have sizes and no memory."""
+    big = 2**32 + 64
+
+    def t(*shape, dtype=torch.bfloat16):
+        return torch.empty(*shape, dtype=dtype, device="meta")
+
+    x, w, off = t(4, 64), t(2, 32, 64), t(3, dtype=torch.int32)
+    for call in (
+        lambda: moe.moe_grouped_gemm(t(big, 64), off, w),
+        lambda: moe.moe_grouped_gemm(t(4, big), off, w),
+        lambda: moe.moe_grouped_gemm(x, None, t(big, 64)),
+        lambda: moe.moe_grouped_gemm(x, off, t(big, 1, 64)),
+        lambda: moe.moe_grouped_gemm_dgrad(t(big, 32), off, w),
+        lambda: moe.moe_grouped_gemm_wgrad(t(big, 64), t(big, 64), off),
+        lambda: moe.moe_quantize_fp8(t(big, 64)),
+        lambda: moe.moe_quantize_fp8(t(4, big), swiglu=True),
+        lambda: moe.moe_grouped_gemm_fp8(t(big, 64, dtype=torch.uint8), t(big, 1, dtype=torch.float32), off,
+                                         t(2, 32, 64, dtype=torch.uint8), t(2, 32, 1, dtype=torch.float32)),
+    ):
+        with pytest.raises(ValueError, match="below 2.31"):
+            call()
