@@ -1049,9 +1049,10 @@ static moe_status gemm_launch(const GemmArgs &a, int nsm, cudaStream_t st) {
     p.stages = std::min<int>(kGemmMaxStages, (kSmemMax - 1024 - gemm_smem_bytes<FP8, BN>(a.E)) / STAGE);
     p.m_tiles = (p.M + 128 * CG - 1) / (128 * CG);
     // The tensor core truncates as it adds, an error that grows with the length of the sum: fp32
-    // results add up parts of 512 in rounded fp32 (K = 4096: 4.4e-6 off in the 2-norm without), bf16
-    // ones, whose rounding is 2^-9, parts of 8192 (about 9e-6). It also bounds what the epilogue
-    // waits for at a time, whatever K or an expert's rows.
+    // results add up parts of 512 in rounded fp32 (K = 4096: 4.4e-6 off in the 2-norm without, 4.8e-7
+    // with; operands of one sign 1.1e-5 and 7e-7), bf16 ones, whose rounding is up to 2^-8, parts of
+    // 8192 (about 9e-6; of one sign 4e-5 too small). It also bounds what the epilogue waits for at a
+    // time, whatever K or an expert's rows.
     p.part = p.out_fp32 ? 8 : 128;
     const size_t smem = (size_t)p.stages * STAGE + gemm_smem_bytes<FP8, BN>(a.E) + 1024;
     constexpr auto kern = [] {

@@ -337,8 +337,9 @@ moe_status moe_quantize_fp8(const void *x, int64_t ldx, int rows, int K, int swi
  *   xq, xs: as moe_quantize_fp8 writes them; wq: E4M3 [E][N][K]; ws: fp32
  *   [E][N][ceil(K/128)], the MOE_FP8_E4M3_K128 experts' arrays in the STANDARD
  *   layout. ldx, ldw, w_estride in bytes; ws_estride in floats (0 = dense).
- *   Each block's sum is formed by the tensor core and added in fp32, with its
- *   scales, to the running sum. y: bf16, or fp32 if y_is_fp32. */
+ *   Each block's sum is formed by the tensor core, multiplied by xs in fp32 (which
+ *   must not overflow: it cannot for xs up to 1.3e31) and added, times ws, to the
+ *   running sum. y: bf16, or fp32 if y_is_fp32. */
 moe_status moe_grouped_gemm_fp8(const void *xq, int64_t ldx, const float *xs, int n_rows, const int32_t *offsets,
                                 const void *wq, int64_t ldw, int64_t w_estride, const float *ws, int64_t ws_estride,
                                 int E, int N, int K, void *y, int64_t ldy, int y_is_fp32, moe_stream_t stream);

@@ -1,5 +1,5 @@
 """Edges of the grouped products and of the FP8 quantiser: values next to fp32's smallest, signed zeros, experts
-without rows."""
+without rows, the accuracy of long sums."""
 import pytest
 import torch
 
@@ -105,3 +105,74 @@ def test_accumulating_leaves_experts_without_rows_as_they_are(moe, counts, N, K)
             want = before[e].double() + dy[at:at + n].double().T @ x[at:at + n].double()
             assert torch.equal(dw[e].double(), want)
         at += n
+
+
+# ---------------------------------------------------------------------------- accuracy of long sums
+
+
+def _off(got, want64):
+    return float((got.double() - want64).norm() / want64.norm())
+
+
+# columns of the result and rows per expert: tiles of single CTAs, and CTA pairs
+SUMS = [([20], 520), ([300, 301, 255, 0, 513, 100, 1, 700], 2056)]
+C = 4096
+
+
+@pytest.mark.parametrize("positive", [False, True])
+@pytest.mark.parametrize("counts,cols", SUMS)
+def test_fp32_sums_are_as_exact_as_parts_of_512_make_them(moe, counts, cols, positive):
+    """The tensor core cuts the sum off after each step of 16 products: by half a unit in the last place on
+    average, which is ln 2 * 2^-24 of the sum on average over a binade, and by a unit at most. (The products
+    have 16 bits and a part's sum is at most 2^9 of them, so aligning them with it cuts hardly any.) Around 0
+    the sum grows like the square root of the steps: over the 32 steps of a part of 512 it loses no more than
+    0.69 * 2^-24 * 2/3 * 32 = 9e-7 of its size were every step to err the same way; parts err by
+    themselves, and adding up eight of them in rounded fp32 is below 2e-7: 1.5e-6. One part of 4096 lost
+    4.4e-6. Positive operands grow like the steps and all parts err downwards: a whole unit a step is
+    2^-23 * 16.5 = 2.0e-6, with the roundings 2.5e-6; a single part would lose half a unit in 256 steps,
+    0.69 * 2^-24 * 128 = 5.3e-6."""
+    g = _gen(2)
+    bound = 2.5e-6 if positive else 1.5e-6
+    draw = torch.rand if positive else torch.randn
+    E, R, off = len(counts), sum(counts), _offsets(counts)
+    at = [0] + torch.tensor(counts).cumsum(0).tolist()
+    x = draw(R, C, generator=g, device="cuda").to(BF16)
+    w = draw(E, cols, C, generator=g, device="cuda").to(BF16)
+    want = torch.cat([x[at[e]:at[e + 1]].double() @ w[e].double().T for e in range(E)])
+    wt = w.transpose(1, 2).contiguous()
+    assert _off(moe.moe_grouped_gemm(x, off, w, y_fp32=True), want) < bound
+    assert _off(moe.moe_grouped_gemm_dgrad(x, off, wt, dx_fp32=True), want) < bound
+
+
+@pytest.mark.parametrize("positive", [False, True])
+@pytest.mark.parametrize("counts,N,K", [([4096], 200, 264), ([4100, 4096], 2056, 1160)])
+def test_fp32_weight_gradients_are_as_exact_as_parts_of_512_make_them(moe, counts, N, K, positive):
+    """As above, the sum running over an expert's rows."""
+    g = _gen(3)
+    draw = torch.rand if positive else torch.randn
+    R = sum(counts)
+    dy = draw(R, N, generator=g, device="cuda").to(BF16)
+    x = draw(R, K, generator=g, device="cuda").to(BF16)
+    dw = moe.moe_grouped_gemm_wgrad(dy, x, _offsets(counts))
+    at = 0
+    for e, n in enumerate(counts):
+        assert _off(dw[e], dy[at:at + n].double().T @ x[at:at + n].double()) < (2.5e-6 if positive else 1.5e-6)
+        at += n
+
+
+def test_bf16_results_of_long_sums_lean_to_no_side(moe):
+    """Positive operands, 2^18 rows: bf16 results add up parts of 8192. Each of a part's 512 steps cuts the
+    sum and, that far above them, its 16 products too, each by half a unit at most on average:
+    17 * 0.69 * 2^-24 * 256 = 1.8e-4 of the sum. Rounding to bf16 is off by up to 2^-8, 1.66e-3 in the root
+    mean square, and leans to no side, so the mean over 256 * 256 results deviates by 6.5e-6: three of them
+    make 2e-4. One part of 2^18 would lose more, half a unit of the sum alone in 2^14 steps:
+    0.69 * 2^-24 * 2^13 = 3.4e-4."""
+    g = _gen(4)
+    R, N, K = 1 << 18, 256, 256
+    dy = torch.rand(R, N, generator=g, device="cuda")
+    dy = (dy * torch.exp2(torch.rand(N, generator=g, device="cuda") * 4)).to(BF16)   # results spread over binades
+    x = torch.rand(R, K, generator=g, device="cuda")
+    x = (x * torch.exp2(torch.rand(K, generator=g, device="cuda") * 4)).to(BF16)
+    want = dy.double().T @ x.double()
+    rel = (moe.moe_grouped_gemm_wgrad(dy, x, None, dw_fp32=False)[0].double() - want) / want
+    assert abs(float(rel.mean())) < 2e-4 and float(rel.abs().max()) <= 2.0**-8 + 2e-4
