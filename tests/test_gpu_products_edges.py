@@ -1,5 +1,6 @@
 """Edges of the grouped products and of the FP8 quantiser: values next to fp32's smallest, signed zeros, experts
-without rows, the accuracy of long sums."""
+without rows, the accuracy of long sums, sizes that
+strides of 16 bytes do not divide, 1024 experts, calls at once."""
 import pytest
 import torch
 
@@ -176,3 +177,106 @@ def test_bf16_results_of_long_sums_lean_to_no_side(moe):
     want = dy.double().T @ x.double()
     rel = (moe.moe_grouped_gemm_wgrad(dy, x, None, dw_fp32=False)[0].double() - want) / want
     assert abs(float(rel.mean())) < 2e-4 and float(rel.abs().max()) <= 2.0**-8 + 2e-4
+
+
+# ---------------------------------------------------------------------------- sizes
+
+
+def _ints(g, rows, cols, *experts, unit=8):
+    """Whole numbers in rows whose stride is a multiple of `unit` and whose padding is NaN."""
+    wide = torch.full((*experts, rows, -(-cols // unit) * unit), float("nan"), dtype=BF16, device="cuda")
+    wide[..., :cols] = torch.randint(-3, 4, (*experts, rows, cols), generator=g, device="cuda").to(BF16)
+    return wide[..., :cols]
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("K,N", [(1, 1), (5, 3), (3, 129), (131, 7), (577, 257), (1025, 2049)])
+@pytest.mark.parametrize("counts", [[1, 0, 2], [37, 0, 5, 300]])
+def test_odd_sizes_in_every_direction(moe, counts, K, N, fp32):
+    g = _gen(5)
+    E, R, off = len(counts), sum(counts), _offsets(counts)
+    at = [0] + torch.tensor(counts).cumsum(0).tolist()
+    parts = [slice(at[e], at[e + 1]) for e in range(E)]
+    x, dy, w = _ints(g, R, K), _ints(g, R, N), _ints(g, N, K, E)
+    dt = torch.float32 if fp32 else BF16
+
+    def same(got, want64):
+        assert got.dtype == dt and torch.equal(got, want64.float().to(dt))
+
+    same(moe.moe_grouped_gemm(x, off, w, y_fp32=fp32), torch.cat([x[p].double() @ w[e].double().T for e, p in enumerate(parts)]))
+    same(moe.moe_grouped_gemm_dgrad(dy, off, w, dx_fp32=fp32), torch.cat([dy[p].double() @ w[e].double() for e, p in enumerate(parts)]))
+    same(moe.moe_grouped_gemm_wgrad(dy, x, off, dw_fp32=fp32), torch.stack([dy[p].double().T @ x[p].double() for p in parts]))
+    # fp8: codes of the same whole numbers, NaN behind K
+    KB = -(-K // 128)
+
+    def codes(t):
+        wide = torch.full((*t.shape[:-1], -(-K // 16) * 16), 0x7F, dtype=torch.uint8, device="cuda")
+        wide[..., :K] = t.float().to(torch.float8_e4m3fn).view(torch.uint8)
+        return wide[..., :K]
+
+    xs = torch.exp2(torch.randint(-3, 2, (R, KB), generator=g, device="cuda").float())
+    ws = torch.exp2(torch.randint(-3, 2, (E, N, KB), generator=g, device="cuda").float())
+    xf = x.double() * xs.double().repeat_interleave(128, dim=-1)[..., :K]
+    wf = w.double() * ws.double().repeat_interleave(128, dim=-1)[..., :K]
+    same(moe.moe_grouped_gemm_fp8(codes(x), xs, off, codes(w), ws, y_fp32=fp32),
+         torch.cat([xf[p] @ wf[e].T for e, p in enumerate(parts)]))
+
+
+def test_as_many_experts_as_there_may_be(moe):
+    """1024 experts, of which the first, the last and a few between have rows."""
+    g = _gen(6)
+    counts = [0] * 1024
+    for e, n in ((0, 3), (31, 1), (32, 70), (500, 2), (991, 40), (1023, 5)):
+        counts[e] = n
+    R, K, N, off = sum(counts), 72, 40, _offsets(counts)
+    x, dy, w = _ints(g, R, K), _ints(g, R, N), _ints(g, N, K, 1024)
+    e = torch.arange(1024, device="cuda").repeat_interleave(torch.tensor(counts, device="cuda"))
+    w64 = w[e].double()
+    assert torch.equal(moe.moe_grouped_gemm(x, off, w, y_fp32=True).double(), torch.einsum("rk,rnk->rn", x.double(), w64))
+    assert torch.equal(moe.moe_grouped_gemm_dgrad(dy, off, w, dx_fp32=True).double(), torch.einsum("rn,rnk->rk", dy.double(), w64))
+    dw = torch.zeros(1024, N, K, dtype=torch.float64, device="cuda")
+    dw.index_add_(0, e, torch.einsum("rn,rk->rnk", dy.double(), x.double()))
+    assert torch.equal(moe.moe_grouped_gemm_wgrad(dy, x, off).double(), dw)
+    codes = torch.zeros(R, 80, dtype=torch.uint8, device="cuda")[:, :K]
+    codes.copy_(x.float().to(torch.float8_e4m3fn).view(torch.uint8))
+    wq = torch.zeros(1024, N, 80, dtype=torch.uint8, device="cuda")[..., :K]
+    wq.copy_(w.float().to(torch.float8_e4m3fn).view(torch.uint8))
+    one = lambda *s: torch.ones(*s, 1, device="cuda")
+    got = moe.moe_grouped_gemm_fp8(codes, one(R), off, wq, one(1024, N), y_fp32=True)
+    assert torch.equal(got.double(), torch.einsum("rk,rnk->rn", x.double(), w64))
+
+
+def test_two_streams_and_two_threads_at_once(moe):
+    """Products of all kinds under way together, from two host threads on two streams, on shared inputs."""
+    import threading
+
+    g = _gen(7)
+    counts, K, N = [300, 301, 255, 0, 513, 100, 1, 700], 512, 1032
+    R, off = sum(counts), _offsets(counts)
+    x, dy, w = _ints(g, R, K), _ints(g, R, N), _ints(g, N, K, len(counts))
+    wq, ws = moe.moe_quantize_fp8(w.reshape(-1, K))
+    wq, ws = wq.view(len(counts), N, K), ws.view(len(counts), N, -1)
+
+    def step():
+        xq, xs = moe.moe_quantize_fp8(x)
+        y = moe.moe_grouped_gemm_fp8(xq, xs, off, wq, ws)
+        return [moe.moe_grouped_gemm(x, off, w), moe.moe_grouped_gemm_dgrad(dy, off, w), moe.moe_grouped_gemm_wgrad(dy, x, off),
+                xq, xs, y, *moe.moe_quantize_fp8(y[:, :1024].contiguous(), swiglu=True)]
+
+    want = step()
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def run(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got[i] = step()
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for outs in got:
+        assert len(outs) == len(want) and all(torch.equal(a, b) for a, b in zip(outs, want))
