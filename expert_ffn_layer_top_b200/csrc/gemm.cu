@@ -20,7 +20,6 @@
 // by TMA in the 128-byte swizzle, and nothing is transposed or copied beforehand.
 #include "common.cuh"
 #include "internal.h"
-#include "mx_codec.cuh"
 #include <type_traits>
 
 namespace moe {
