@@ -326,7 +326,8 @@ _INT_MAX = 2**31 - 1   # sizes are C ints, which ctypes fills with a larger numb
 
 
 # The wrappers below are called for every projection of a decode step, where their own time is
-# most of a small product's: each tensor's shape and strides are asked for once.
+# most of a small product's: each tensor's shape and strides are asked for once. Like the layer's
+# they hand addresses to the library, so autograd records none of them: results require no gradient.
 
 
 def _device(t: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
@@ -408,7 +409,8 @@ def _result(out: Optional[torch.Tensor], rows: int, cols: int, fp32: bool, devic
 
 def moe_grouped_gemm(x: torch.Tensor, offsets: Optional[torch.Tensor], w: torch.Tensor, y_fp32: bool = False,
                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """y[r] = w[e] x[r] for the rows r of expert e; w bf16 [E, N, K] (or [N, K] with offsets None)."""
+    """y[r] = w[e] x[r] for the rows r of expert e; w bf16 [E, N, K] (or [N, K] with offsets None). Not recorded
+    by autograd: moe_grouped_gemm_dgrad and moe_grouped_gemm_wgrad are its gradients."""
     rows, cols, ldx = _matrix("x", x, _BF16)
     E, N, K, ldw, es = _batch("w", w, _BF16)
     if cols != K:
